@@ -46,6 +46,16 @@ SIGNATURES = {
     "moe_permute_noalloc": [_P, _I, _I, _I, _P, _P, _P, _P, _P],
     "moe_plan_stage_ms": [_P, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int), _I],
     "moe_route_margin_quantiles": [_P, _P, _P, _I, ctypes.POINTER(ctypes.c_double), _I, _P, _P],
+    "moe_add_rmsnorm_mxfp8": [_P, _P, _I, _P, ctypes.c_float, _I, _I, _P, _P, _P, _P, _P],
+    "moe_linear_create": [_I, _I, _I, ctypes.POINTER(_P)],
+    "moe_linear_workspace_bytes": [_P, ctypes.POINTER(_S)],
+    "moe_linear_set_workspace": [_P, _P, _S],
+    "moe_linear_check": [_P, _P, ctypes.POINTER(ctypes.c_uint)],
+    "moe_linear_destroy": [_P],
+    "moe_linear_bytes": [_I, _I, ctypes.POINTER(_S), ctypes.POINTER(_S)],
+    "moe_pack_linear_mxfp4": [_I, _I, _P, _P, _P],
+    "moe_linear_mxfp4": [_P, _P, _P, _I, _P, _P, _I, _P],
+    "moe_forward_decode": [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P],
     "moe_quantile_balance": [_P, _P, _P, _I, ctypes.POINTER(ctypes.c_double), _I, BIAS_RULE, _P, _P, _P],
 }
 
@@ -75,6 +85,10 @@ class LatentBF16(ctypes.Structure):
     _fields_ = [("w_down", _P), ("gamma", _P), ("w_up", _P)]
 
 
+class MatrixMXFP4(ctypes.Structure):
+    _fields_ = [("w", _P), ("s", _P)]
+
+
 _lib = None
 
 
@@ -102,6 +116,38 @@ def _call(name, *args):
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _checked(name, t, dtype, shape, device):
+    """t's data pointer, after checks that a pointer alone cannot carry: type, shape, contiguity, device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+class _OnDevice:
+    """The device of a call's tensors made current, and its stream the one that new outputs
+    belong to (a no-op where both already are)."""
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {device}")
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
 
 
 def _stream(stream=None):
@@ -249,6 +295,123 @@ def moe_pack_shared_bf16(d, I_shared, w_gate, w_up, w_down, shared, stream=None)
           _stream(stream))
 
 
+MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
+_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
+
+
+def _type(name, dtype):
+    if dtype not in _TYPES:
+        raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {dtype}")
+    return _TYPES[dtype]
+
+
+def moe_add_rmsnorm_mxfp8(x, gamma, eps=1e-5, residual=None, residual_out=None, xn=None, q=None, scale=None,
+                          with_xn=True, with_mx=True, stream=None):
+    """r = x + residual (x alone without one), the RMSNorm of r as bf16 and as MXFP8.
+
+    x: bf16 [rows, cols]; gamma: fp32 [cols]; residual: bf16 or fp32 [rows, cols] or None.
+    Returns (r in the residual's type or None, xn bf16, q uint8 [rows, cols], scale uint8
+    [rows, cols / 32]).  Outputs are allocated where not given; residual_out may be the residual
+    itself.  with_xn / with_mx = False leave xn / (q, scale) out (None)."""
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [rows, cols], got {tuple(x.shape)}")
+    rows, cols = x.shape
+    dev = x.device
+    rtype = MOE_TYPE_BF16 if residual is None else _type("residual", residual.dtype)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if (xn is not None and not with_xn) or ((q is not None or scale is not None) and not with_mx):
+        raise ValueError("an output was given that with_xn / with_mx leave out")
+    with _OnDevice(dev, stream):
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+        if with_xn and xn is None:
+            xn = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        if with_mx:
+            q = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if q is None else q
+            scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev) if scale is None else scale
+        _call("moe_add_rmsnorm_mxfp8", _checked("x", x, torch.bfloat16, (rows, cols), dev),
+              _checked("residual", residual, residual.dtype if residual is not None else None, (rows, cols), dev), rtype,
+              _checked("gamma", gamma, torch.float32, (cols,), dev), eps, rows, cols,
+              _checked("residual_out", residual_out, residual.dtype if residual is not None else None, (rows, cols), dev),
+              _checked("xn", xn, torch.bfloat16, (rows, cols), dev),
+              _checked("q", q, torch.uint8, (rows, cols), dev),
+              _checked("scale", scale, torch.uint8, (rows, cols // 32), dev), _stream(stream))
+    return residual_out, xn, q, scale
+
+
+def moe_linear_create(T_max, N, K):
+    h = ctypes.c_void_p()
+    _call("moe_linear_create", T_max, N, K, ctypes.byref(h))
+    return h
+
+
+def moe_linear_workspace_bytes(linear):
+    n = ctypes.c_size_t()
+    _call("moe_linear_workspace_bytes", linear, ctypes.byref(n))
+    return n.value
+
+
+def moe_linear_set_workspace(linear, ws):
+    _call("moe_linear_set_workspace", linear, _ptr(ws), ws.numel() * ws.element_size())
+
+
+def moe_linear_check(linear, stream=None):
+    bits = ctypes.c_uint()
+    code = lib().moe_linear_check(linear, _stream(stream), ctypes.byref(bits))
+    return code, bits.value
+
+
+def moe_linear_destroy(linear):
+    _call("moe_linear_destroy", linear)
+
+
+def moe_linear_bytes(N, K):
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _call("moe_linear_bytes", N, K, ctypes.byref(a), ctypes.byref(b))
+    return a.value, b.value
+
+
+def moe_pack_linear_mxfp4(N, K, w, weights, stream=None):
+    with _OnDevice(w.device, None):
+        _call("moe_pack_linear_mxfp4", N, K, _checked("w", w, torch.float32, (N, K), weights.w.device),
+              ctypes.byref(weights.struct()), _stream(stream))
+
+
+def moe_linear_mxfp4(linear, q, scale, weights, y=None, dtype=torch.bfloat16, stream=None):
+    """y [T, N] (bf16 or fp32) = W x for MXFP8 rows q uint8 [T, K], scale uint8 [T, K / 32] and a
+    LinearMXFP4 on `linear`, a handle of moe_linear_create for its shape."""
+    N, K, dev = weights.N, weights.K, weights.w.device
+    T = q.shape[0]
+    with _OnDevice(dev, stream):
+        if y is None:
+            y = torch.empty((T, N), dtype=dtype, device=dev)
+        _call("moe_linear_mxfp4", linear, _checked("q", q, torch.uint8, (T, K), dev),
+              _checked("scale", scale, torch.uint8, (T, K // 32), dev), T, ctypes.byref(weights.struct()),
+              _checked("y", y, y.dtype, (T, N), dev), _type("y", y.dtype), _stream(stream))
+    return y
+
+
+def moe_forward_decode(plan, x, idx, w, experts, shared=None, q=None, scale=None, y=None, stream=None):
+    """The layer for up to 8 tokens x bf16 [T, d]; (q, scale) is their MXFP8 form where it is at
+    hand, and x may then be None without a shared expert."""
+    T, d = (q if x is None else x).shape
+    dev = idx.device
+    k = idx.shape[1] if idx.dim() == 2 else -1
+    ex = experts.struct()
+    sh = shared.struct() if shared is not None else None
+    with _OnDevice(dev, stream):
+        if y is None:
+            y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+        _call("moe_forward_decode", plan, _checked("x", x, torch.bfloat16, (T, experts.d), dev),
+              _checked("q", q, torch.uint8, (T, experts.d), dev),
+              _checked("scale", scale, torch.uint8, (T, experts.d // 32), dev), T,
+              _checked("idx", idx, torch.int32, (T, k), dev), _checked("w", w, torch.float32, (T, k), dev),
+              ctypes.byref(ex), ctypes.byref(sh) if sh is not None else None,
+              _checked("y", y, torch.bfloat16, (T, d), dev), _stream(stream))
+    return y
+
+
 def moe_debug_buffer(plan, which):
     """(device pointer, bytes) of a workspace buffer (see include/moe.h)."""
     p, n = ctypes.c_void_p(), ctypes.c_size_t()
@@ -317,6 +480,49 @@ class Shared:
                              w_down.contiguous(), self, stream)
 
 
+class LinearMXFP4:
+    """Device buffers of a packed MXFP4 matrix [N, K] (allocated by torch)."""
+
+    def __init__(self, N, K, device="cuda"):
+        self.N, self.K = N, K
+        self.w, self.s = (torch.empty(n, dtype=torch.uint8, device=device) for n in moe_linear_bytes(N, K))
+
+    def struct(self):
+        return MatrixMXFP4(self.w.data_ptr(), self.s.data_ptr())
+
+    def pack(self, w, stream=None):
+        moe_pack_linear_mxfp4(self.N, self.K, w.contiguous(), self, stream)
+
+
+class LinearPlan:
+    """A handle for MXFP4 linears of one shape plus its torch-allocated workspace."""
+
+    def __init__(self, T_max, N, K, device="cuda"):
+        self.T_max, self.N, self.K = T_max, N, K
+        self.handle = None
+        with torch.cuda.device(device):
+            self.handle = moe_linear_create(T_max, N, K)
+            self.workspace = torch.empty(moe_linear_workspace_bytes(self.handle), dtype=torch.uint8, device=device)
+            moe_linear_set_workspace(self.handle, self.workspace)
+
+    def forward(self, q, scale, weights, y=None, dtype=torch.bfloat16, stream=None):
+        if (weights.N, weights.K) != (self.N, self.K) or weights.w.device != self.workspace.device:
+            raise ValueError(f"weights [{weights.N}, {weights.K}] on {weights.w.device}: the plan is for [{self.N}, {self.K}] "
+                             f"on {self.workspace.device}")
+        return moe_linear_mxfp4(self.handle, q, scale, weights, y, dtype, stream)
+
+    def check(self, stream=None):
+        return moe_linear_check(self.handle, stream)
+
+    def __del__(self):
+        try:
+            if getattr(self, "handle", None) is not None:
+                moe_linear_destroy(self.handle)
+                self.handle = None
+        except Exception:
+            pass
+
+
 MOE_ACT_SILU_GLU, MOE_ACT_CLAMPED_SWIGLU = 0, 1
 MOE_BIAS_LOGIT, MOE_BIAS_SELECT_ONLY = 0, 1
 MOE_FLAG_STATIC_ROUTER = 1
@@ -359,6 +565,16 @@ class Plan:
         if self.d_latent:
             return moe_forward_latent(self.handle, x, idx, w, latent, experts, shared, y, stream)
         return moe_forward(self.handle, x, idx, w, experts, shared, y, stream)
+
+    def forward_decode(self, x, idx, w, experts, shared=None, q=None, scale=None, y=None, stream=None):
+        """forward for up to 8 tokens, from their MXFP8 form (q, scale) where it is given."""
+        if (experts.d, experts.I, experts.E, idx.shape[-1]) != (self.d, self.I, self.E, self.k):
+            raise ValueError(f"experts d={experts.d} I={experts.I} E={experts.E}, idx {tuple(idx.shape)}: the plan has "
+                             f"d={self.d} I={self.I} E={self.E} k={self.k}")
+        if shared is not None and (shared.d, shared.I_shared) != (self.d, self.I_shared):
+            raise ValueError(f"shared expert d={shared.d} I_shared={shared.I_shared}: the plan has d={self.d} "
+                             f"I_shared={self.I_shared}")
+        return moe_forward_decode(self.handle, x, idx, w, experts, shared, q, scale, y, stream)
 
     def check(self, stream=None):
         return moe_plan_check(self.handle, stream)

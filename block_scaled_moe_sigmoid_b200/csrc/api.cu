@@ -12,7 +12,9 @@
 #include "../../include/moe.h"
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
+#include "few.cuh"
 #include "kernels.cuh"
+#include "norm.cuh"
 #include "router.cuh"
 
 using namespace moe;
@@ -157,7 +159,7 @@ struct moe_plan_s {
   // workspace carve (byte offsets)
   size_t o_status, o_chunk, o_counts, o_offsets, o_tiles, o_perm, o_inv, o_logits, o_zpart,
       o_planes, o_xq, o_xs_tok, o_xs, o_hq, o_hs, o_O, o_hsh, o_ys, o_spart, o_theta, o_qbuf, o_xl, o_xn, o_yl,
-      o_yr, total;
+      o_yr, o_fcnt, o_fpart, o_himg, total;
   int dl = 0;              // latent option: expert width (0 = off)
   float eps_lat = 1e-5f;
   int tokens_per_chunk() const { return kPermThreads; }
@@ -208,6 +210,11 @@ static void carve(moe_plan_s* p) {
   } else {
     p->o_xl = p->o_xn = p->o_yl = p->o_yr = 0;
   }
+  // few-token calls: tile counters and fp32 partials of two ragged tiles per CTA, and the
+  // MXFP8 rows between the two expert products
+  p->o_fcnt = take((size_t)kFewMaxCtas * 4);
+  p->o_fpart = take((size_t)2 * kFewMaxCtas * kFewPart * 4);
+  p->o_himg = take((size_t)std::min(p->T_max, kFewRows) * p->k * (p->I / 128) * kFewHRow);
   p->total = o;
 }
 
@@ -318,8 +325,8 @@ static cudaError_t launch_gemm(int bn, const GemmArgs& a, const CUtensorMap& tA,
 // would fill less than half the SMs (few tokens), split K so that up to one CTA runs per SM,
 // keeping at least 4 K tiles per split and the fp32 partials (ksplit * elems) within the
 // workspace.  1 = no split.  No split is empty: (ks - 1) * ceil(k_tiles / ks) < k_tiles.
-static int dense_ksplit(const moe_plan_s* p, int tiles, int k_tiles, size_t elems) {
-  const int cap = std::min(p->num_sms, kSplitMaxCtas);
+static int dense_ksplit(int num_sms, int tiles, int k_tiles, size_t elems) {
+  const int cap = std::min(num_sms, kSplitMaxCtas);
   if (tiles <= 0 || 2 * tiles > cap) return 1;
   int ks = std::min(cap / tiles, k_tiles / 4);
   while (ks > 1 && (size_t)ks * elems > (size_t)kSplitMaxCtas * kBN * 256) --ks;
@@ -415,6 +422,7 @@ moe_status_t moe_plan_set_workspace(moe_plan_t p, void* dev_ptr, size_t bytes) {
   p->ws_bytes = bytes;
   p->planes_of = nullptr;   // the router planes live in the workspace
   if (cudaMemset(p->ws + p->o_status, 0, 256) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaMemset(p->ws + p->o_fcnt, 0, (size_t)kFewMaxCtas * 4) != cudaSuccess) return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
@@ -425,6 +433,8 @@ moe_status_t moe_plan_check(moe_plan_t p, void* stream, unsigned int* bits) {
   if (cudaStreamSynchronize(S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemcpy(&v, p->ws + p->o_status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemset(p->ws + p->o_status, 0, 4) != cudaSuccess) return MOE_ERR_CUDA;
+  // a kernel that gave up may have left a tile counter behind
+  if (v && cudaMemset(p->ws + p->o_fcnt, 0, (size_t)kFewMaxCtas * 4) != cudaSuccess) return MOE_ERR_CUDA;
   if (bits) *bits = v;
   if (v & MOE_DEV_ERR_TIMEOUT) return MOE_ERR_TIMEOUT;
   if (v) return MOE_ERR_DEVICE_FAULT;
@@ -595,6 +605,96 @@ static cudaError_t dense_bf16_f32(const moe_plan_s* p, const void* W, int M, con
   return launch_gemm<KIND_BF16, EPI_F32>(bn, a, tA, tB, std::min(tiles, p->num_sms), s);
 }
 
+// a8: the shared expert (bf16) on every token: *ys = its fp32 output [T][d], NULL without one.
+static moe_status_t run_shared(moe_plan_s* p, const void* x, int T, const moe_shared_bf16* sh, int dbn,
+                               cudaStream_t s, float** ys_out) {
+  *ys_out = nullptr;
+  p->last_shared_split = p->last_shared_split_dn = 0;
+  if (!sh) return MOE_OK;
+  const int d = p->d, Is = p->Is;
+  __nv_bfloat16* hsh = p->at<__nv_bfloat16>(p->o_hsh);
+  float* ys = p->at<float>(p->o_ys);
+  CUtensorMap tA;
+  BMaps tB;
+  if (!make_map(&tA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sh->w_gu, d, 2ull * Is, (uint64_t)d * 2, 64, 256) ||
+      !make_bmaps(&tB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, d, T, (uint64_t)d * 2, 64))
+    return MOE_ERR_CUDA;
+  GemmArgs a = base_args(p);
+  a.dense_rows = T;
+  a.num_groups = 1;
+  a.M_total = 2 * Is;
+  a.m_tiles = 2 * Is / 256;
+  a.k_tiles = d / 64;
+  a.kb_wrap = a.k_tiles;
+  a.B_rows = T;
+  a.out0 = hsh;
+  a.ld_out = Is;
+  int tiles = ((T + dbn - 1) / dbn) * a.m_tiles;
+  float* spart = p->at<float>(p->o_spart);
+  p->prof.begin(MOE_STAGE_SHARED_GATE_UP, s);
+  const int ks_gu = dense_ksplit(p->num_sms, tiles, a.k_tiles, (size_t)T * 2 * Is);
+  if (ks_gu > 1) {
+    // few token tiles: split K over the SMs, fp32 partials, then sum + GLU + bf16
+    a.ksplit = ks_gu;
+    a.k_per = (a.k_tiles + ks_gu - 1) / ks_gu;
+    a.split_stride = (long long)T * 2 * Is;
+    a.out0 = spart;
+    a.ld_out = 2 * Is;
+    if (launch_gemm<KIND_BF16, EPI_F32>(dbn, a, tA, tB, std::min(tiles * ks_gu, p->num_sms), s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    const long long n = (long long)T * Is;
+    if (p->act == MOE_ACT_CLAMPED_SWIGLU)
+      launch_k(split_glu_reduce_kernel<1>, (unsigned)((n + 255) / 256), 256, 0, s, spart, ks_gu, T, Is, a.split_stride, hsh);
+    else
+      launch_k(split_glu_reduce_kernel<0>, (unsigned)((n + 255) / 256), 256, 0, s, spart, ks_gu, T, Is, a.split_stride, hsh);
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+  } else {
+    const cudaError_t e = p->act == MOE_ACT_CLAMPED_SWIGLU
+        ? launch_gemm<KIND_BF16, EPI_GLU_BF16_CLAMPED>(dbn, a, tA, tB, std::min(tiles, p->num_sms), s)
+        : launch_gemm<KIND_BF16, EPI_GLU_BF16>(dbn, a, tA, tB, std::min(tiles, p->num_sms), s);
+    if (e != cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  p->last_shared_split = ks_gu;
+  p->prof.end(s);
+  CUtensorMap tA2;
+  BMaps tB2;
+  if (!make_map(&tA2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sh->w_dn, Is, d, (uint64_t)Is * 2, 64, 256) ||
+      !make_bmaps(&tB2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, hsh, Is, T, (uint64_t)Is * 2, 64))
+    return MOE_ERR_CUDA;
+  GemmArgs b = base_args(p);
+  b.dense_rows = T;
+  b.num_groups = 1;
+  b.M_total = d;
+  b.m_tiles = (d + 255) / 256;
+  b.k_tiles = Is / 64;
+  b.kb_wrap = b.k_tiles;
+  b.B_rows = T;
+  b.out0 = ys;
+  b.ld_out = d;
+  tiles = ((T + dbn - 1) / dbn) * b.m_tiles;
+  p->prof.begin(MOE_STAGE_SHARED_DOWN, s);
+  const int ks_dn = dense_ksplit(p->num_sms, tiles, b.k_tiles, (size_t)T * d);
+  if (ks_dn > 1) {
+    b.ksplit = ks_dn;
+    b.k_per = (b.k_tiles + ks_dn - 1) / ks_dn;
+    b.split_stride = (long long)T * d;
+    b.out0 = spart;
+    if (launch_gemm<KIND_BF16, EPI_F32>(dbn, b, tA2, tB2, std::min(tiles * ks_dn, p->num_sms), s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    const long long n = (long long)T * d;
+    launch_k(split_sum_kernel, (unsigned)((n + 255) / 256), 256, 0, s, spart, ks_dn, n, b.split_stride, ys);
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+  } else {
+    if (launch_gemm<KIND_BF16, EPI_F32>(dbn, b, tA2, tB2, std::min(tiles, p->num_sms), s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  p->last_shared_split_dn = ks_dn;
+  p->prof.end(s);
+  *ys_out = ys;
+  return MOE_OK;
+}
+
 static moe_status_t forward_impl(moe_plan_t p, const void* x, int T, const int32_t* idx, const float* w,
                                  const moe_latent_bf16* lat, const moe_experts_mxfp4* ex,
                                  const moe_shared_bf16* sh, void* y, void* stream) {
@@ -616,7 +716,7 @@ static moe_status_t forward_impl(moe_plan_t p, const void* x, int T, const int32
   if (lat && (!aligned(lat->w_down, 16) || !aligned(lat->w_up, 16) || !aligned(lat->gamma, 4)))
     return MOE_ERR_ALIGNMENT;
   cudaStream_t s = S(stream);
-  const int d = p->d, E = p->E, k = p->k, I = p->I, Is = p->Is;
+  const int d = p->d, E = p->E, k = p->k, I = p->I;
   const int de = lat ? p->dl : d;   // width the routed experts act on
   const int A = T * k;
   const int bn = p->tile_rows(T);                    // routed GEMM tiles
@@ -717,89 +817,8 @@ static moe_status_t forward_impl(moe_plan_t p, const void* x, int T, const int32
   }
   // a8: shared expert (bf16)
   float* ys = nullptr;
-  if (sh) {
-    __nv_bfloat16* hsh = p->at<__nv_bfloat16>(p->o_hsh);
-    ys = p->at<float>(p->o_ys);
-    CUtensorMap tA;
-    BMaps tB;
-    if (!make_map(&tA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sh->w_gu, d, 2ull * Is, (uint64_t)d * 2, 64, 256) ||
-        !make_bmaps(&tB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, d, T, (uint64_t)d * 2, 64))
-      return MOE_ERR_CUDA;
-    GemmArgs a = base_args(p);
-    a.dense_rows = T;
-    a.num_groups = 1;
-    a.M_total = 2 * Is;
-    a.m_tiles = 2 * Is / 256;
-    a.k_tiles = d / 64;
-    a.kb_wrap = a.k_tiles;
-    a.B_rows = T;
-    a.out0 = hsh;
-    a.ld_out = Is;
-    int tiles = ((T + dbn - 1) / dbn) * a.m_tiles;
-    float* spart = p->at<float>(p->o_spart);
-    p->prof.begin(MOE_STAGE_SHARED_GATE_UP, s);
-    const int ks_gu = dense_ksplit(p, tiles, a.k_tiles, (size_t)T * 2 * Is);
-    if (ks_gu > 1) {
-      // few token tiles: split K over the SMs, fp32 partials, then sum + GLU + bf16
-      a.ksplit = ks_gu;
-      a.k_per = (a.k_tiles + ks_gu - 1) / ks_gu;
-      a.split_stride = (long long)T * 2 * Is;
-      a.out0 = spart;
-      a.ld_out = 2 * Is;
-      if (launch_gemm<KIND_BF16, EPI_F32>(dbn, a, tA, tB, std::min(tiles * ks_gu, p->num_sms), s) != cudaSuccess)
-        return MOE_ERR_CUDA;
-      const long long n = (long long)T * Is;
-      if (p->act == MOE_ACT_CLAMPED_SWIGLU)
-        launch_k(split_glu_reduce_kernel<1>, (unsigned)((n + 255) / 256), 256, 0, s, spart, ks_gu, T, Is, a.split_stride, hsh);
-      else
-        launch_k(split_glu_reduce_kernel<0>, (unsigned)((n + 255) / 256), 256, 0, s, spart, ks_gu, T, Is, a.split_stride, hsh);
-      if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    } else {
-      const cudaError_t e = p->act == MOE_ACT_CLAMPED_SWIGLU
-          ? launch_gemm<KIND_BF16, EPI_GLU_BF16_CLAMPED>(dbn, a, tA, tB, std::min(tiles, p->num_sms), s)
-          : launch_gemm<KIND_BF16, EPI_GLU_BF16>(dbn, a, tA, tB, std::min(tiles, p->num_sms), s);
-      if (e != cudaSuccess)
-        return MOE_ERR_CUDA;
-    }
-    p->last_shared_split = ks_gu;
-    p->prof.end(s);
-    CUtensorMap tA2;
-    BMaps tB2;
-    if (!make_map(&tA2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sh->w_dn, Is, d, (uint64_t)Is * 2, 64, 256) ||
-        !make_bmaps(&tB2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, hsh, Is, T, (uint64_t)Is * 2, 64))
-      return MOE_ERR_CUDA;
-    GemmArgs b = base_args(p);
-    b.dense_rows = T;
-    b.num_groups = 1;
-    b.M_total = d;
-    b.m_tiles = (d + 255) / 256;
-    b.k_tiles = Is / 64;
-    b.kb_wrap = b.k_tiles;
-    b.B_rows = T;
-    b.out0 = ys;
-    b.ld_out = d;
-    tiles = ((T + dbn - 1) / dbn) * b.m_tiles;
-    p->prof.begin(MOE_STAGE_SHARED_DOWN, s);
-    const int ks_dn = dense_ksplit(p, tiles, b.k_tiles, (size_t)T * d);
-    if (ks_dn > 1) {
-      b.ksplit = ks_dn;
-      b.k_per = (b.k_tiles + ks_dn - 1) / ks_dn;
-      b.split_stride = (long long)T * d;
-      b.out0 = spart;
-      if (launch_gemm<KIND_BF16, EPI_F32>(dbn, b, tA2, tB2, std::min(tiles * ks_dn, p->num_sms), s) != cudaSuccess)
-        return MOE_ERR_CUDA;
-      const long long n = (long long)T * d;
-      launch_k(split_sum_kernel, (unsigned)((n + 255) / 256), 256, 0, s, spart, ks_dn, n, b.split_stride, ys);
-      if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-    } else {
-      if (launch_gemm<KIND_BF16, EPI_F32>(dbn, b, tA2, tB2, std::min(tiles, p->num_sms), s) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    }
-    p->last_shared_split_dn = ks_dn;
-    p->prof.end(s);
-  } else {
-    p->last_shared_split = p->last_shared_split_dn = 0;
-  }
+  const moe_status_t st_sh = run_shared(p, x, T, sh, dbn, s, &ys);
+  if (st_sh != MOE_OK) return st_sh;
   if (!lat) {
     // a9: weighted combine with the shared output
     p->prof.begin(MOE_STAGE_COMBINE, s);
@@ -1123,3 +1142,5 @@ extern "C" moe_status_t moe_permute_noalloc(const int32_t* idx, int T, int E, in
                                                                          chunk, perm_tok, inv);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
+
+#include "decode_api.cuh"

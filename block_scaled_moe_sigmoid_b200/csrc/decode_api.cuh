@@ -1,0 +1,334 @@
+// C ABI of the operators around a decode step (include/moe.h): the norm before the layer, MXFP4
+// linears, and the layer for a few tokens.  Included by api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+// A tile-major MXFP4 matrix array as rows of 64 bytes, in boxes of 256 rows with the 64-byte
+// swizzle (few.cuh): one box is one contiguous 16 KB tile.
+bool make_few_map(CUtensorMap* m, const void* base, uint64_t rows) {
+  EncodeTiledFn f = encode_fn();
+  if (!f) return false;
+  cuuint64_t dims[2] = {64, rows};
+  cuuint64_t strides[1] = {64};
+  cuuint32_t box[2] = {64, 256};
+  cuuint32_t es[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launch few_kernel on up to one CTA per SM, with as many pipeline stages as fit.
+template <int MODE, int ACT>
+cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, int grid, cudaStream_t s) {
+  auto kern = few_kernel<MODE, ACT>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = ensure_smem_attr(kern, kFewSmemMax, done);
+  if (e != cudaSuccess) return e;
+  const int stage = few_smem(MODE, a.T, a.k, a.K, 1).total - few_smem(MODE, a.T, a.k, a.K, 0).total;
+  const int room = kFewSmemMax - few_smem(MODE, a.T, a.k, a.K, 0).total;
+  a.stages = std::min(kFewMaxStages, room / stage);
+  if (a.stages < 3) return cudaErrorInvalidValue;
+  return launch_k(kern, grid, kFewThreads, few_smem(MODE, a.T, a.k, a.K, a.stages).total, s, a, tW);
+}
+
+// The dense block-scaled GEMM in its two token-tile configurations.
+template <int EPI>
+cudaError_t launch_linear_gemm(int bn, const GemmArgs& a, const CUtensorMap& tA, const BMaps& tB, int grid, cudaStream_t s) {
+  if (bn == kBNSmall) return launch_gemm_cfg<KIND_MX, EPI, kBNSmall, kStagesSmall>(a, tA, tB, grid, s);
+  return launch_gemm_cfg<KIND_MX, EPI, kBN, kStages>(a, tA, tB, grid, s);
+}
+
+}  // namespace
+
+struct moe_linear_s {
+  int T_max, N, K;
+  int num_sms = 148;
+  char* ws = nullptr;
+  size_t o_status, o_cnt, o_part, o_xs, o_split, split_floats, total;
+  template <class P>
+  P* at(size_t off) const { return (P*)(ws + off); }
+  bool few(int T) const { return T <= kFewRows && (long long)T * K <= kFewMaxX; }
+  // token rows per tile of the GEMM path
+  static int tile_rows(int T) { return T <= 64 ? kBNSmall : kBN; }
+};
+
+extern "C" {
+
+moe_status_t moe_add_rmsnorm_mxfp8(const void* x, const void* residual, moe_type_t residual_type, const float* gamma,
+                                   float eps, int rows, int cols, void* residual_out, void* xn, uint8_t* q,
+                                   uint8_t* scale, void* stream) {
+  if (rows < 0 || cols <= 0 || !(eps > 0.0f) || (residual_type != MOE_TYPE_BF16 && residual_type != MOE_TYPE_F32))
+    return MOE_ERR_INVALID_ARG;
+  if (cols % 32 || cols > kNormMaxCols) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return MOE_OK;
+  if ((residual_out && !residual) || (q != nullptr) != (scale != nullptr) || !(residual_out || xn || q))
+    return MOE_ERR_INVALID_ARG;
+  if (!x || !gamma) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(residual_out, 16) || !aligned(xn, 16) ||
+      !aligned(q, 16))
+    return MOE_ERR_ALIGNMENT;
+  NormArgs a{(const uint16_t*)x, residual, gamma, eps, rows, cols, residual_out, (uint16_t*)xn, q, scale};
+  const int nvec = cols / 8;
+  const int V = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4;
+  const int team = ((nvec + V - 1) / V + 31) / 32 * 32;
+  const int per_cta = std::max(1, 128 / team);
+  const dim3 block(team, per_cta);
+  const unsigned grid = (unsigned)((rows + per_cta - 1) / per_cta);
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto kern) { e = launch_k(kern, grid, block, 0, S(stream), a); };
+  const int res = !residual ? NORM_RES_NONE : residual_type == MOE_TYPE_BF16 ? NORM_RES_BF16 : NORM_RES_F32;
+  switch (res * 8 + V) {
+    case NORM_RES_NONE * 8 + 1: go(add_rmsnorm_mxfp8_kernel<NORM_RES_NONE, 1>); break;
+    case NORM_RES_NONE * 8 + 2: go(add_rmsnorm_mxfp8_kernel<NORM_RES_NONE, 2>); break;
+    case NORM_RES_NONE * 8 + 4: go(add_rmsnorm_mxfp8_kernel<NORM_RES_NONE, 4>); break;
+    case NORM_RES_BF16 * 8 + 1: go(add_rmsnorm_mxfp8_kernel<NORM_RES_BF16, 1>); break;
+    case NORM_RES_BF16 * 8 + 2: go(add_rmsnorm_mxfp8_kernel<NORM_RES_BF16, 2>); break;
+    case NORM_RES_BF16 * 8 + 4: go(add_rmsnorm_mxfp8_kernel<NORM_RES_BF16, 4>); break;
+    case NORM_RES_F32 * 8 + 1: go(add_rmsnorm_mxfp8_kernel<NORM_RES_F32, 1>); break;
+    case NORM_RES_F32 * 8 + 2: go(add_rmsnorm_mxfp8_kernel<NORM_RES_F32, 2>); break;
+    default: go(add_rmsnorm_mxfp8_kernel<NORM_RES_F32, 4>); break;
+  }
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- MXFP4 linear
+moe_status_t moe_linear_create(int T_max, int N, int K, moe_linear_t* out) {
+  if (!out) return MOE_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (T_max < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  const long long m_tiles = ((long long)N + 255) / 256;
+  // tensor-map coordinates are 32-bit: tile rows of the weights, and token rows
+  if (K % 128 || m_tiles * (K / 128) * 256 > (1ll << 30) || T_max > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  moe_linear_s* p = new moe_linear_s();
+  p->T_max = T_max; p->N = N; p->K = K;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && sms > 0)
+    p->num_sms = sms;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t r = o; o = up(o + bytes, 1024); return r; };
+  p->o_status = take(256);
+  p->o_cnt = take((size_t)kFewMaxCtas * 4);
+  p->o_part = take((size_t)2 * kFewMaxCtas * kFewPart * 4);
+  // GEMM path: token scale blocks, and the partials of a split K (at most kSplitMaxCtas tiles of
+  // at most kBN x 256, and no more splits than K / 512)
+  p->o_xs = take(((size_t)T_max / kBNMin + 2) * (K / 128) * SF_TILE_BYTES);
+  p->split_floats = std::min((size_t)kSplitMaxCtas * kBN * 256, (size_t)(K / 512) * T_max * N);
+  p->o_split = take(p->split_floats * 4);
+  p->total = o;
+  *out = p;
+  return MOE_OK;
+}
+
+moe_status_t moe_linear_workspace_bytes(moe_linear_t p, size_t* bytes) {
+  if (!p || !bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = p->total;
+  return MOE_OK;
+}
+
+moe_status_t moe_linear_set_workspace(moe_linear_t p, void* dev_ptr, size_t bytes) {
+  if (!p || !dev_ptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dev_ptr, 256)) return MOE_ERR_ALIGNMENT;
+  if (bytes < p->total) return MOE_ERR_INVALID_ARG;
+  p->ws = (char*)dev_ptr;
+  // the status word and the tile counters
+  if (cudaMemset(p->ws, 0, p->o_part) != cudaSuccess) return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+moe_status_t moe_linear_check(moe_linear_t p, void* stream, unsigned int* bits) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
+  unsigned int v = 0;
+  if (cudaStreamSynchronize(S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaMemcpy(&v, p->ws + p->o_status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
+  // a kernel that gave up may have left a tile counter behind
+  if (v && cudaMemset(p->ws, 0, p->o_part) != cudaSuccess) return MOE_ERR_CUDA;
+  if (bits) *bits = v;
+  if (v & MOE_DEV_ERR_TIMEOUT) return MOE_ERR_TIMEOUT;
+  if (v) return MOE_ERR_DEVICE_FAULT;
+  return MOE_OK;
+}
+
+moe_status_t moe_linear_destroy(moe_linear_t p) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  delete p;
+  return MOE_OK;
+}
+
+moe_status_t moe_linear_bytes(int N, int K, size_t* w, size_t* s) {
+  if (N <= 0 || K <= 0 || !w || !s) return MOE_ERR_INVALID_ARG;
+  if (K % 128) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const size_t tiles = ((size_t)N + 255) / 256 * (K / 128);
+  *w = tiles * kFewTile;
+  *s = tiles * 1024;
+  return MOE_OK;
+}
+
+moe_status_t moe_pack_linear_mxfp4(int N, int K, const float* src, const moe_matrix_mxfp4* dst, void* stream) {
+  size_t nw = 0, ns = 0;
+  if (!src || !dst || !dst->w || !dst->s) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = moe_linear_bytes(N, K, &nw, &ns);
+  if (st != MOE_OK) return st;
+  if (!aligned(src, 16) || !aligned(dst->w, 256) || !aligned(dst->s, 16)) return MOE_ERR_ALIGNMENT;
+  const long long n = (long long)N * (K / 32);
+  if ((n + 255) / 256 > 0x7fffffffll) return MOE_ERR_UNSUPPORTED_SHAPE;
+  cudaStream_t s = S(stream);
+  // rows past N in the last 256-row tile are zeros
+  if (N % 256 && (cudaMemsetAsync(dst->w, 0, nw, s) != cudaSuccess || cudaMemsetAsync(dst->s, 0, ns, s) != cudaSuccess))
+    return MOE_ERR_CUDA;
+  pack_mxfp4_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(src, nullptr, N, K, 0, (uint8_t*)dst->w, (uint8_t*)dst->s);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* scale, int T, const moe_matrix_mxfp4* W,
+                              void* y, moe_type_t y_type, void* stream) {
+  if (!p || T < 0 || (y_type != MOE_TYPE_BF16 && y_type != MOE_TYPE_F32)) return MOE_ERR_INVALID_ARG;
+  if (T > p->T_max) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!q || !scale || !W || !W->w || !W->s || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(scale, 4) || !aligned(W->w, 256) || !aligned(W->s, 16) || !aligned(y, 16))
+    return MOE_ERR_ALIGNMENT;
+  if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
+  cudaStream_t s = S(stream);
+  const int N = p->N, K = p->K, k_tiles = K / 128, m_tiles = (N + 255) / 256;
+  if (p->few(T)) {
+    CUtensorMap tW;
+    if (!make_few_map(&tW, W->w, (uint64_t)m_tiles * k_tiles * 256)) return MOE_ERR_CUDA;
+    FewArgs a;
+    memset(&a, 0, sizeof(a));
+    a.T = T;
+    a.m_tiles = m_tiles;
+    a.k_tiles = k_tiles;
+    a.rows = N;
+    a.K = K;
+    a.sf = (const uint8_t*)W->s;
+    a.xq = q;
+    a.xs = scale;
+    a.y = y;
+    a.y_f32 = y_type == MOE_TYPE_F32;
+    a.part = p->at<float>(p->o_part);
+    a.counters = p->at<unsigned int>(p->o_cnt);
+    a.status = p->at<unsigned int>(p->o_status);
+    const int grid = (int)std::min<long long>((long long)m_tiles * k_tiles, std::min(p->num_sms, kFewMaxCtas));
+    return launch_few<FEW_LINEAR, 0>(a, tW, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  // more rows: the block-scaled GEMM on one dense group
+  const int bn = moe_linear_s::tile_rows(T), nt = (T + bn - 1) / bn;
+  uint8_t* xs = p->at<uint8_t>(p->o_xs);
+  if (launch_k(linear_scale_tiles_kernel, dim3(nt, std::min(k_tiles, 8)), 256, 0, s, scale, T, bn, k_tiles, xs) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  CUtensorMap tA;
+  BMaps tB;
+  if (!make_map(&tA, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, W->w, 128, (uint64_t)m_tiles * k_tiles * 256, 64, 128, 256) ||
+      !make_bmaps(&tB, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, T, K, 128))
+    return MOE_ERR_CUDA;
+  GemmArgs a;
+  memset(&a, 0, sizeof(a));
+  a.status = p->at<unsigned int>(p->o_status);
+  a.ksplit = 1;
+  a.dense_rows = T;
+  a.num_groups = 1;
+  a.M_total = N;
+  a.m_tiles = m_tiles;
+  a.k_tiles = k_tiles;
+  a.kb_wrap = k_tiles;
+  a.B_rows = T;
+  a.sfa = (const uint8_t*)W->s;
+  a.a_ptr = (const uint8_t*)W->w;
+  a.sfb = xs;
+  a.out0 = y;
+  a.ld_out = N;
+  const long long tiles = (long long)nt * m_tiles;
+  if (tiles > 0x7fffffffll) return MOE_ERR_UNSUPPORTED_SHAPE;
+  int ks = tiles > kSplitMaxCtas ? 1 : dense_ksplit(p->num_sms, (int)tiles, k_tiles, (size_t)T * N);
+  if ((size_t)ks * T * N > p->split_floats) ks = 1;
+  const int grid = (int)std::min<long long>(tiles * ks, p->num_sms);
+  cudaError_t e;
+  if (ks > 1) {
+    a.ksplit = ks;
+    a.k_per = (k_tiles + ks - 1) / ks;
+    a.split_stride = (long long)T * N;
+    float* part = p->at<float>(p->o_split);
+    a.out0 = part;
+    e = launch_linear_gemm<EPI_F32>(bn, a, tA, tB, grid, s);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    const long long n = (long long)T * N;
+    if (y_type == MOE_TYPE_F32)
+      e = launch_k(split_sum_kernel, (unsigned)((n + 255) / 256), 256, 0, s, part, ks, n, a.split_stride, (float*)y);
+    else
+      e = launch_k(split_sum_bf16_kernel, (unsigned)((n + 255) / 256), 256, 0, s, part, ks, n, a.split_stride,
+                   (__nv_bfloat16*)y);
+  } else if (y_type == MOE_TYPE_F32) {
+    e = launch_linear_gemm<EPI_F32>(bn, a, tA, tB, grid, s);
+  } else {
+    e = launch_linear_gemm<EPI_BF16>(bn, a, tA, tB, grid, s);
+  }
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- the layer for a few tokens
+moe_status_t moe_forward_decode(moe_plan_t p, const void* x, const uint8_t* q, const uint8_t* scale, int T,
+                                const int32_t* idx, const float* w, const moe_experts_mxfp4* ex,
+                                const moe_shared_bf16* sh, void* y, void* stream) {
+  if (!p || T < 0 || p->dl > 0) return MOE_ERR_INVALID_ARG;   // no latent form
+  if (T > p->T_max || T > kFewRows || (long long)T * p->d > kFewMaxX) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return MOE_OK;
+  if ((q != nullptr) != (scale != nullptr) || (!x && (!q || p->Is > 0))) return MOE_ERR_INVALID_ARG;
+  if (!idx || !w || !ex || !y || !ex->w_gu || !ex->s_gu || !ex->w_dn || !ex->s_dn) return MOE_ERR_INVALID_ARG;
+  if ((p->Is > 0) != (sh != nullptr) || (sh && (!sh->w_gu || !sh->w_dn))) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(y, 16) || !aligned(idx, 4) || !aligned(w, 4) ||
+      !aligned(ex->w_gu, 256) || !aligned(ex->w_dn, 256) || !aligned(ex->s_gu, 16) || !aligned(ex->s_dn, 16) ||
+      (sh && (!aligned(sh->w_gu, 16) || !aligned(sh->w_dn, 16))))
+    return MOE_ERR_ALIGNMENT;
+  if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
+  cudaStream_t s = S(stream);
+  const int d = p->d, E = p->E, I = p->I;
+  float* ys = nullptr;
+  const moe_status_t st = run_shared(p, x, T, sh, kBNSmall, s, &ys);
+  if (st != MOE_OK) return st;
+  FewArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = T;
+  a.k = p->k;
+  a.E = E;
+  a.idx = idx;
+  a.w = w;
+  a.himg = p->at<uint8_t>(p->o_himg);
+  a.part = p->at<float>(p->o_fpart);
+  a.counters = p->at<unsigned int>(p->o_fcnt);
+  a.status = p->at<unsigned int>(p->o_status);
+  const int grid = std::min(p->num_sms, kFewMaxCtas);
+  CUtensorMap tW;
+  // gate/up, GLU, MXFP8 rows of the hidden values
+  a.m_tiles = I / 128;
+  a.k_tiles = d / 128;
+  a.K = d;
+  a.sf = (const uint8_t*)ex->s_gu;
+  a.x = q ? nullptr : (const uint16_t*)x;
+  a.xq = q;
+  a.xs = scale;
+  if (!make_few_map(&tW, ex->w_gu, (uint64_t)E * a.m_tiles * a.k_tiles * 256)) return MOE_ERR_CUDA;
+  p->prof.begin(MOE_STAGE_GATE_UP, s);
+  if ((p->act == MOE_ACT_CLAMPED_SWIGLU ? launch_few<FEW_GLU, 1>(a, tW, grid, s) : launch_few<FEW_GLU, 0>(a, tW, grid, s)) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  p->prof.end(s);
+  // down, weighted combine, shared output
+  a.m_tiles = (d + 255) / 256;
+  a.k_tiles = I / 128;
+  a.rows = d;
+  a.K = I;
+  a.sf = (const uint8_t*)ex->s_dn;
+  a.ys = ys;
+  a.y = y;
+  if (!make_few_map(&tW, ex->w_dn, (uint64_t)E * a.m_tiles * a.k_tiles * 256)) return MOE_ERR_CUDA;
+  p->prof.begin(MOE_STAGE_DOWN, s);
+  if (launch_few<FEW_DOWN, 0>(a, tW, grid, s) != cudaSuccess) return MOE_ERR_CUDA;
+  p->prof.end(s);
+  p->last_T = T;
+  return MOE_OK;
+}
+
+}  // extern "C"

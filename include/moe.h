@@ -260,6 +260,72 @@ moe_status_t moe_forward_latent(moe_plan_t plan, const void* x_bf16, int T, cons
                                 const moe_experts_mxfp4* experts, const moe_shared_bf16* shared,
                                 void* y_bf16, void* stream);
 
+/* ---- element types of the calls below --------------------------------------------------- */
+typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type_t;
+
+/* ---- residual addition, RMSNorm and MXFP8 quantisation -----------------------------------
+ * What stands before the layer in every block, in one kernel:
+ *   r  = x + residual, rounded to the residual's type; r = x without a residual
+ *   n  = r / sqrt(mean(r^2) + eps) * gamma            (per row; sums in fp32)
+ *   xn = bf16(n);  (q, scale) = moe_quant_mxfp8(xn), byte for byte
+ * x_bf16: device bf16 [rows][cols]; residual: device [rows][cols] of residual_type, or NULL;
+ * gamma: device fp32 [cols]; residual_out: r in residual_type, or NULL (may be `residual`
+ * itself); xn_bf16: device bf16 [rows][cols] or NULL; q_e4m3 / scale_e8m0: as
+ * moe_quant_mxfp8's, or both NULL.  At least one output.  xn feeds moe_route, moe_forward and
+ * the shared expert, (q, scale) feed moe_linear_mxfp4 and moe_forward_decode.
+ * cols % 32 == 0, cols <= 32768; eps > 0; every pointer but scale 16-byte aligned.  The sum of
+ * squares is an fp32 sum: rows whose |r| passes about 2^56 overflow it.  rows = 0 is a no-op. */
+moe_status_t moe_add_rmsnorm_mxfp8(const void* x_bf16, const void* residual, moe_type_t residual_type,
+                                   const float* gamma, float eps, int rows, int cols, void* residual_out,
+                                   void* xn_bf16, uint8_t* q_e4m3, uint8_t* scale_e8m0, void* stream);
+
+/* ---- MXFP4 linear --------------------------------------------------------------------------
+ * y[t] = W x[t] for a weight matrix W [N][K] in MXFP4 and rows x in MXFP8 (both with one E8M0
+ * scale per 32 elements along K, accumulation in fp32).  Up to 8 rows (and T K <= 80 KB) run as
+ * a stream of the weights over all SMs, more rows on the tensor cores' block-scaled GEMM; both
+ * read the same packed weights.
+ * moe_linear_create: a host object for calls of up to T_max rows on matrices of one shape;
+ * N >= 1, K % 128 == 0, and at most 2^30 / 256 tiles of 256 x 128.  Workspace, check and destroy
+ * as for moe_plan_*: caller-owned device memory, one call at a time per object. */
+typedef struct moe_linear_s* moe_linear_t;
+/* A packed matrix (device pointers; w 256-byte, s 16-byte aligned), in the tile-major layout of
+ * the experts: w E2M1 codes [ceil(N/256)][K/128][256][64 B], s E8M0 scales
+ * [ceil(N/256)][K/128][2][512]; rows past N are zero.  Scale bytes 0 to 254. */
+typedef struct {
+  void* w;
+  void* s;
+} moe_matrix_mxfp4;
+moe_status_t moe_linear_create(int T_max, int N, int K, moe_linear_t* out);
+moe_status_t moe_linear_workspace_bytes(moe_linear_t linear, size_t* bytes);
+moe_status_t moe_linear_set_workspace(moe_linear_t linear, void* dev_ptr, size_t bytes);
+moe_status_t moe_linear_check(moe_linear_t linear, void* stream, unsigned int* device_bits);
+moe_status_t moe_linear_destroy(moe_linear_t linear);
+/* Byte sizes of a packed matrix (host outputs). */
+moe_status_t moe_linear_bytes(int N, int K, size_t* w, size_t* s);
+/* MXFP4-quantise fp32 W (device [N][K], 16-byte aligned) into `dst`, as moe_pack_expert_mxfp4. */
+moe_status_t moe_pack_linear_mxfp4(int N, int K, const float* w, const moe_matrix_mxfp4* dst, void* stream);
+/* q_e4m3: device [T][K] (16-byte aligned); scale_e8m0: device [T][K/32] (4-byte aligned); y:
+ * device [T][N] of y_type (16-byte aligned).  0 <= T <= T_max; T = 0 is a no-op. */
+moe_status_t moe_linear_mxfp4(moe_linear_t linear, const uint8_t* q_e4m3, const uint8_t* scale_e8m0, int T,
+                              const moe_matrix_mxfp4* weights, void* y, moe_type_t y_type, void* stream);
+
+/* ---- the layer for a few tokens -------------------------------------------------------------
+ * moe_forward's layer for 1 <= T <= 8 tokens of a decode step, from the same packed experts: the
+ * gate/up and down products stream the touched experts' weights once, split evenly over the SMs,
+ * instead of running one tile per expert.  The same roundings as moe_forward except that the
+ * experts' outputs are summed in fp32 (moe_forward holds each in bf16).
+ * x_bf16: device [T][d], read by the shared expert and, without q, quantised to MXFP8; it may be
+ * NULL when q is given and the plan has no shared expert.  q_e4m3 / scale_e8m0: device [T][d] /
+ * [T][d/32], the MXFP8 form of the tokens (moe_add_rmsnorm_mxfp8, moe_quant_mxfp8), or both NULL.
+ * Other arguments as moe_forward.  An id outside [0, E) contributes nothing and is flagged
+ * (MOE_ERR_DEVICE_FAULT at moe_plan_check); an expert that a token names twice counts with the
+ * sum of both weights.  T <= 8, T d <= 80 KB; not for latent plans (MOE_ERR_INVALID_ARG).  Uses the
+ * plan workspace (one call at a time per plan). */
+moe_status_t moe_forward_decode(moe_plan_t plan, const void* x_bf16, const uint8_t* q_e4m3,
+                                const uint8_t* scale_e8m0, int T, const int32_t* idx, const float* w,
+                                const moe_experts_mxfp4* experts, const moe_shared_bf16* shared, void* y_bf16,
+                                void* stream);
+
 /* ---- setup helpers (not on the timed path) --------------------------------------------
  * Byte sizes of the four packed expert arrays for E experts (host outputs). */
 moe_status_t moe_expert_bytes(int d, int I, int E, size_t* w_gu, size_t* s_gu, size_t* w_dn,
