@@ -393,7 +393,7 @@ def moe_linear_mxfp4(linear, q, scale, weights, y=None, dtype=torch.bfloat16, st
 
 
 def moe_forward_decode(plan, x, idx, w, experts, shared=None, q=None, scale=None, y=None, stream=None):
-    """The layer for up to 8 tokens x bf16 [T, d]; (q, scale) is their MXFP8 form where it is at
+    """The layer for up to 16 tokens x bf16 [T, d]; (q, scale) is their MXFP8 form where it is at
     hand, and x may then be None without a shared expert."""
     T, d = (q if x is None else x).shape
     dev = idx.device
@@ -567,7 +567,7 @@ class Plan:
         return moe_forward(self.handle, x, idx, w, experts, shared, y, stream)
 
     def forward_decode(self, x, idx, w, experts, shared=None, q=None, scale=None, y=None, stream=None):
-        """forward for up to 8 tokens, from their MXFP8 form (q, scale) where it is given."""
+        """forward for up to 16 tokens, from their MXFP8 form (q, scale) where it is given."""
         if (experts.d, experts.I, experts.E, idx.shape[-1]) != (self.d, self.I, self.E, self.k):
             raise ValueError(f"experts d={experts.d} I={experts.I} E={experts.E}, idx {tuple(idx.shape)}: the plan has "
                              f"d={self.d} I={self.I} E={self.E} k={self.k}")

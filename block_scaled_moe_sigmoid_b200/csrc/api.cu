@@ -159,7 +159,7 @@ struct moe_plan_s {
   // workspace carve (byte offsets)
   size_t o_status, o_chunk, o_counts, o_offsets, o_tiles, o_perm, o_inv, o_logits, o_zpart,
       o_planes, o_xq, o_xs_tok, o_xs, o_hq, o_hs, o_O, o_hsh, o_ys, o_spart, o_theta, o_qbuf, o_xl, o_xn, o_yl,
-      o_yr, o_fcnt, o_fpart, o_himg, total;
+      o_yr, o_fcnt, o_fpart, o_fhq, o_fhs, total;
   int dl = 0;              // latent option: expert width (0 = off)
   float eps_lat = 1e-5f;
   int tokens_per_chunk() const { return kPermThreads; }
@@ -214,7 +214,9 @@ static void carve(moe_plan_s* p) {
   // MXFP8 rows between the two expert products
   p->o_fcnt = take((size_t)kFewMaxCtas * 4);
   p->o_fpart = take((size_t)2 * kFewMaxCtas * kFewPart * 4);
-  p->o_himg = take((size_t)std::min(p->T_max, kFewRows) * p->k * (p->I / 128) * kFewHRow);
+  const size_t few_T = (size_t)std::min(p->T_max, kFewRows);
+  p->o_fhq = take(few_T * p->k * few_T * p->I);
+  p->o_fhs = take(few_T * p->k * (p->I / 128) * 512);
   p->total = o;
 }
 

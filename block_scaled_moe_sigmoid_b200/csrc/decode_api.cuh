@@ -4,32 +4,24 @@
 
 namespace {
 
-// A tile-major MXFP4 matrix array as rows of 64 bytes, in boxes of 256 rows with the 64-byte
-// swizzle (few.cuh): one box is one contiguous 16 KB tile.
-bool make_few_map(CUtensorMap* m, const void* base, uint64_t rows) {
-  EncodeTiledFn f = encode_fn();
-  if (!f) return false;
-  cuuint64_t dims[2] = {64, rows};
-  cuuint64_t strides[1] = {64};
-  cuuint32_t box[2] = {64, 256};
-  cuuint32_t es[2] = {1, 1};
-  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// The weights' and the token rows' maps of few_kernel: tile-major weights as the grouped GEMM reads them,
+// token rows in boxes of 16.
+bool make_few_maps(CUtensorMap* mW, CUtensorMap* mX, const void* w, uint64_t tiles, const void* x, uint64_t rows, int K) {
+  return make_map(mW, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, w, 128, tiles * 256, 64, 128, 256) &&
+         make_map(mX, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, K, rows, K, 128, kFewRows);
 }
 
-// Launch few_kernel on up to one CTA per SM, with as many pipeline stages as fit.
+// Launch few_kernel with as many pipeline stages as fit.
 template <int MODE, int ACT>
-cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, int grid, cudaStream_t s) {
+cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, const CUtensorMap& tX, int grid, cudaStream_t s) {
   auto kern = few_kernel<MODE, ACT>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_attr(kern, kFewSmemMax, done);
   if (e != cudaSuccess) return e;
-  const int stage = few_smem(MODE, a.T, a.k, a.K, 1).total - few_smem(MODE, a.T, a.k, a.K, 0).total;
-  const int room = kFewSmemMax - few_smem(MODE, a.T, a.k, a.K, 0).total;
-  a.stages = std::min(kFewMaxStages, room / stage);
+  const int fixed = few_smem(MODE, a.T, a.k, a.k_tiles, 0).total;
+  a.stages = std::min(kFewMaxStages, (kFewSmemMax - fixed) / (kFewStage + kFewSF));
   if (a.stages < 3) return cudaErrorInvalidValue;
-  return launch_k(kern, grid, kFewThreads, few_smem(MODE, a.T, a.k, a.K, a.stages).total, s, a, tW);
+  return launch_k(kern, grid, kFewThreads, few_smem(MODE, a.T, a.k, a.k_tiles, a.stages).total, s, a, tW, tX);
 }
 
 // The dense block-scaled GEMM in its two token-tile configurations.
@@ -48,7 +40,6 @@ struct moe_linear_s {
   size_t o_status, o_cnt, o_part, o_xs, o_split, split_floats, total;
   template <class P>
   P* at(size_t off) const { return (P*)(ws + off); }
-  bool few(int T) const { return T <= kFewRows && (long long)T * K <= kFewMaxX; }
   // token rows per tile of the GEMM path
   static int tile_rows(int T) { return T <= 64 ? kBNSmall : kBN; }
 };
@@ -193,18 +184,16 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
   if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
   cudaStream_t s = S(stream);
   const int N = p->N, K = p->K, k_tiles = K / 128, m_tiles = (N + 255) / 256;
-  if (p->few(T)) {
-    CUtensorMap tW;
-    if (!make_few_map(&tW, W->w, (uint64_t)m_tiles * k_tiles * 256)) return MOE_ERR_CUDA;
+  if (T <= kFewRows) {
+    CUtensorMap tW, tX;
+    if (!make_few_maps(&tW, &tX, W->w, (uint64_t)m_tiles * k_tiles, q, T, K)) return MOE_ERR_CUDA;
     FewArgs a;
     memset(&a, 0, sizeof(a));
     a.T = T;
     a.m_tiles = m_tiles;
     a.k_tiles = k_tiles;
     a.rows = N;
-    a.K = K;
     a.sf = (const uint8_t*)W->s;
-    a.xq = q;
     a.xs = scale;
     a.y = y;
     a.y_f32 = y_type == MOE_TYPE_F32;
@@ -212,7 +201,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
     a.counters = p->at<unsigned int>(p->o_cnt);
     a.status = p->at<unsigned int>(p->o_status);
     const int grid = (int)std::min<long long>((long long)m_tiles * k_tiles, std::min(p->num_sms, kFewMaxCtas));
-    return launch_few<FEW_LINEAR, 0>(a, tW, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_few<FEW_LINEAR, 0>(a, tW, tX, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   // more rows: the block-scaled GEMM on one dense group
   const int bn = moe_linear_s::tile_rows(T), nt = (T + bn - 1) / bn;
@@ -273,12 +262,12 @@ moe_status_t moe_forward_decode(moe_plan_t p, const void* x, const uint8_t* q, c
                                 const int32_t* idx, const float* w, const moe_experts_mxfp4* ex,
                                 const moe_shared_bf16* sh, void* y, void* stream) {
   if (!p || T < 0 || p->dl > 0) return MOE_ERR_INVALID_ARG;   // no latent form
-  if (T > p->T_max || T > kFewRows || (long long)T * p->d > kFewMaxX) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T > p->T_max || T > kFewRows) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
   if ((q != nullptr) != (scale != nullptr) || (!x && (!q || p->Is > 0))) return MOE_ERR_INVALID_ARG;
   if (!idx || !w || !ex || !y || !ex->w_gu || !ex->s_gu || !ex->w_dn || !ex->s_dn) return MOE_ERR_INVALID_ARG;
   if ((p->Is > 0) != (sh != nullptr) || (sh && (!sh->w_gu || !sh->w_dn))) return MOE_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(y, 16) || !aligned(idx, 4) || !aligned(w, 4) ||
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4) || !aligned(y, 16) || !aligned(idx, 4) || !aligned(w, 4) ||
       !aligned(ex->w_gu, 256) || !aligned(ex->w_dn, 256) || !aligned(ex->s_gu, 16) || !aligned(ex->s_dn, 16) ||
       (sh && (!aligned(sh->w_gu, 16) || !aligned(sh->w_dn, 16))))
     return MOE_ERR_ALIGNMENT;
@@ -295,37 +284,44 @@ moe_status_t moe_forward_decode(moe_plan_t p, const void* x, const uint8_t* q, c
   a.E = E;
   a.idx = idx;
   a.w = w;
-  a.himg = p->at<uint8_t>(p->o_himg);
+  a.hq = p->at<uint8_t>(p->o_fhq);
+  a.hs = p->at<uint8_t>(p->o_fhs);
   a.part = p->at<float>(p->o_fpart);
   a.counters = p->at<unsigned int>(p->o_fcnt);
   a.status = p->at<unsigned int>(p->o_status);
   const int grid = std::min(p->num_sms, kFewMaxCtas);
-  CUtensorMap tW;
+  if (!q) {
+    uint8_t* xq = p->at<uint8_t>(p->o_xq);
+    uint8_t* xs = p->at<uint8_t>(p->o_xs_tok);
+    p->prof.begin(MOE_STAGE_QUANT, s);
+    const moe_status_t sq = moe_quant_mxfp8(x, T, d, xq, xs, stream);
+    if (sq != MOE_OK) return sq;
+    p->prof.end(s);
+    q = xq;
+    scale = xs;
+  }
+  CUtensorMap tW, tX;
   // gate/up, GLU, MXFP8 rows of the hidden values
   a.m_tiles = I / 128;
   a.k_tiles = d / 128;
-  a.K = d;
   a.sf = (const uint8_t*)ex->s_gu;
-  a.x = q ? nullptr : (const uint16_t*)x;
-  a.xq = q;
   a.xs = scale;
-  if (!make_few_map(&tW, ex->w_gu, (uint64_t)E * a.m_tiles * a.k_tiles * 256)) return MOE_ERR_CUDA;
+  if (!make_few_maps(&tW, &tX, ex->w_gu, (uint64_t)E * a.m_tiles * a.k_tiles, q, T, d)) return MOE_ERR_CUDA;
   p->prof.begin(MOE_STAGE_GATE_UP, s);
-  if ((p->act == MOE_ACT_CLAMPED_SWIGLU ? launch_few<FEW_GLU, 1>(a, tW, grid, s) : launch_few<FEW_GLU, 0>(a, tW, grid, s)) !=
-      cudaSuccess)
+  if ((p->act == MOE_ACT_CLAMPED_SWIGLU ? launch_few<FEW_GLU, 1>(a, tW, tX, grid, s)
+                                        : launch_few<FEW_GLU, 0>(a, tW, tX, grid, s)) != cudaSuccess)
     return MOE_ERR_CUDA;
   p->prof.end(s);
   // down, weighted combine, shared output
   a.m_tiles = (d + 255) / 256;
   a.k_tiles = I / 128;
   a.rows = d;
-  a.K = I;
   a.sf = (const uint8_t*)ex->s_dn;
   a.ys = ys;
   a.y = y;
-  if (!make_few_map(&tW, ex->w_dn, (uint64_t)E * a.m_tiles * a.k_tiles * 256)) return MOE_ERR_CUDA;
+  if (!make_few_maps(&tW, &tX, ex->w_dn, (uint64_t)E * a.m_tiles * a.k_tiles, a.hq, (uint64_t)T * a.k * T, I)) return MOE_ERR_CUDA;
   p->prof.begin(MOE_STAGE_DOWN, s);
-  if (launch_few<FEW_DOWN, 0>(a, tW, grid, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_few<FEW_DOWN, 0>(a, tW, tX, grid, s) != cudaSuccess) return MOE_ERR_CUDA;
   p->prof.end(s);
   p->last_T = T;
   return MOE_OK;

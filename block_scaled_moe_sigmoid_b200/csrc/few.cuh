@@ -1,31 +1,31 @@
-// Matrix products with MXFP4 weights for a few token rows (T <= 8): a stream of the weights.
+// Matrix products with MXFP4 weights for a few token rows (T <= 16): a stream of the weights.
 //
 //   FEW_LINEAR  y[t] = W x[t]                                    one matrix, x in MXFP8
-//   FEW_GLU     h[t,j] = MX(glu(Wg x[t], Wu x[t]))               the experts e = idx[t][j]
+//   FEW_GLU     h[t,e] = MX(glu(Wg x[t], Wu x[t]))               the experts e = idx[t][j]
 //   FEW_DOWN    y[t] = bf16(ys[t] + sum_j w[t][j] Wd h[t,j])     the same experts
 //
 // With so few rows every weight byte is used once and the bytes are the cost: 17/32 byte per
 // weight at the copy rate of the memory.  The work is one list of steps, a step being one 256-row
 // x 128-column tile of packed weights (16 KB of codes, one contiguous block, and 1 KB of scales).
 // CTA c of G takes the steps [c S / G, (c + 1) S / G): every SM streams the same number of bytes
-// whatever the number of experts, rows or columns.  Where a CTA's range begins or ends inside a
+// whatever the number of experts, rows or columns.  (The grouped GEMM gives a CTA whole tiles: one
+// token's 16 experts make 384 of them, 2.6 per SM.)  Where a CTA's range begins or ends inside a
 // tile's contraction it writes an fp32 partial, and the CTA that arrives last at the tile's counter
 // adds the partials in the order of the CTAs (a fixed order: results do not depend on timing) and
 // finishes the tile.  No CTA waits for another.
 //
-// FEW_DOWN contracts over (expert, column) in one go: the routing weight is folded into the scale
-// of h, and a token that does not use an expert contributes zeros there, so a tile of y needs no
-// other sum.
+// FEW_DOWN contracts over (expert, column) in one go: a tile of y takes the experts one after the
+// other, each through an accumulator of its own that the epilogue adds, times the token's weight, to
+// fp32 registers.
 //
-// A step's products run on mma.sync m16n8k16 (f16 operands, fp32 accumulation): the 256 weight
-// rows are M, the up to 8 tokens N.  E2M1 and E4M3 values are exact in f16 and so are their products in
-// fp32; each 32-element block is summed on its own and then added to the fp32 accumulator times
-// the two block scales.  tcgen05 would need the 128-row x 128-byte padded operand in shared memory
-// per 64 bytes loaded; with N = 8 the legacy instruction is far from its own limit here.
+// A step's products are eight tcgen05.mma kind::mxf8f6f4.block_scale (two 128-row halves x four
+// 32-column blocks, N = 16 tokens), which decode the codes and apply the scales themselves.  The same
+// products on mma.sync were measured too: making f16 operands out of the codes then takes more than
+// the load (40000 x 7168, 8 rows: cvt 3.0 TB/s, half of it by bit moves 2.6 TB/s, E4M3 operands 2.4 TB/s).
 //
-// Lane (g, c) = (lane / 4, lane % 4) reads 4 bytes = 8 codes of a weight row's block: the fragment's
-// logical k order is permuted the same way on both sides, so that each operand is one load.  The
-// tile is loaded with the 64-byte swizzle, which makes those reads free of bank conflicts.
+// Roles (384 threads): warp 0 loads weight tiles and their scales, warp 10 the token rows (a 16-row
+// box per step), warp 11 moves each step's scales into TMEM, warp 1 issues the MMAs, warps 2 to 9 run
+// the epilogue, a thread per weight row.
 #pragma once
 #include "gemm.cuh"
 #include "kernels.cuh"
@@ -33,33 +33,32 @@
 namespace moe {
 
 enum { FEW_LINEAR = 0, FEW_GLU = 1, FEW_DOWN = 2 };
-constexpr int kFewRows = 8;                    // tokens per call
-constexpr int kFewWarps = 16;                  // consumer warps: 8 row groups x 2 halves of a step's columns
-constexpr int kFewThreads = 32 * (kFewWarps + 1);
+constexpr int kFewRows = 16;                   // tokens per call: the MMA's N
+constexpr int kFewThreads = 384;
 constexpr int kFewTile = 256 * 64;             // bytes of codes per step
-constexpr int kFewHRow = 144;                  // h image: 128 codes, 4 scales, padding, per (pair, K tile)
-constexpr int kFewHStride = 160;               // the same in shared memory: 8 tokens, no bank conflicts
-constexpr int kFewRedStride = 260;             // floats between the tokens of the tile sums
+constexpr int kFewATile = 256 * 128;           // the same in shared memory, a byte per code
+constexpr int kFewBTile = kFewRows * 128;
+constexpr int kFewStage = kFewATile + kFewBTile;
+constexpr int kFewSF = 1024 + 512;             // weight and token scale atoms per stage
+constexpr int kFewMaxStages = 6;
 constexpr int kFewPart = kFewRows * 256;       // floats of a partial
 constexpr int kFewMaxCtas = 256;               // bound on the grid (sizes partials and counters)
-constexpr int kFewMaxStages = 12;
 constexpr int kFewSmemMax = 232448;
-constexpr int kNoSlot = 0x7fffffff;              // the token does not use the expert
-constexpr int kFewMaxX = 80 * 1024;            // bytes of MXFP8 codes a CTA keeps resident
+constexpr int kFewTmemCols = 256;              // two accumulators of 2 x 16 columns, 16 columns of scales per stage
+static_assert(kFewStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
+static_assert(64 + 16 * kFewMaxStages <= kFewTmemCols, "TMEM budget");
 
 struct FewArgs {
   int T, k, E;
   int m_tiles, k_tiles;   // of one matrix
   int rows;               // valid output rows (FEW_LINEAR, FEW_DOWN)
-  int K;                  // columns of x (FEW_LINEAR, FEW_GLU)
   int stages;
   const uint8_t* sf;      // weight scales, [matrix][m-tile][k-tile][1 KB]
   const int* idx;
   const float* w;
-  const uint16_t* x;      // bf16 x, quantised here, or
-  const uint8_t* xq;      // its MXFP8 codes and scales
-  const uint8_t* xs;
-  uint8_t* himg;          // [T k][k-tile of the down product][144]
+  const uint8_t* xs;      // FEW_LINEAR, FEW_GLU: token scales [T][4 k_tiles]
+  uint8_t* hq;            // codes of h, [used expert][T][128 k-tiles of the down product]
+  uint8_t* hs;            // scale atoms of h, [used expert][k-tile][512]
   const float* ys;        // shared expert's output, or NULL
   void* y;
   int y_f32;
@@ -70,19 +69,17 @@ struct FewArgs {
 
 // Shared-memory layout (byte offsets from a 1024-byte aligned base); host and device agree on it.
 struct FewSmem {
-  int sf, xst, red, x, sx, tab, ctrl, total;
+  int sf, ctrl, xs, red, tab, total;
 };
-__host__ __device__ inline FewSmem few_smem(int mode, int T, int k, int K, int stages) {
+__host__ __device__ inline FewSmem few_smem(int mode, int T, int k, int k_tiles, int stages) {
   FewSmem s;
-  int o = stages * kFewTile;
-  s.sf = o; o += stages * 1024;
-  s.xst = o; if (mode == FEW_DOWN) o += stages * kFewRows * kFewHStride;
-  s.red = o; o += kFewRows * kFewRedStride * 4;
-  s.x = o; if (mode != FEW_DOWN) o += T * (K + 32);
-  s.sx = o; if (mode != FEW_DOWN) o += K / 32 * kFewRows * 4;
-  s.tab = o; if (mode != FEW_LINEAR) o += (256 + (3 + 2 * kFewRows) * T * k) * 4;
-  o = (o + 15) & ~15;
-  s.ctrl = o; o += 2 * kFewMaxStages * 8 + 64;
+  int o = stages * kFewStage;
+  s.sf = o; o += stages * kFewSF;
+  s.ctrl = o; o += 512;
+  s.xs = o; if (mode != FEW_DOWN) o += T * k_tiles * 4;              // token scales
+  s.red = o; if (mode == FEW_GLU) o += T * 128 * 4;                  // up values on their way to the gates
+  s.tab = o; if (mode != FEW_LINEAR) o += (256 + 4 * T * k) * 4;     // experts in use
+  if (mode == FEW_DOWN) o += T * k * T * 4;                          // and their tokens' weights
   s.total = o + 1024;
   return s;
 }
@@ -92,97 +89,77 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-// 8 E2M1 codes -> four f16 pairs, in code order
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-// 8 E4M3 codes -> four f16 pairs
-__device__ __forceinline__ void e4m3x8_to_f16(uint2 v, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b16 p0, p1, p2, p3;\n\t"
-      "mov.b32 {p0, p1}, %4;\n\t"
-      "mov.b32 {p2, p3}, %5;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, p0;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, p1;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %2, p2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %3, p3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(v.x), "r"(v.y));
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// E8M0 byte -> 2^(b - 127); b = 0 is the subnormal 2^-127
-__device__ __forceinline__ float e8m0_f32(uint32_t b) { return __uint_as_float(max(b << 23, 0x00400000u)); }
-__device__ __forceinline__ float e8m0_byte_f32(uint32_t word, int j) { return e8m0_f32((word >> (8 * j)) & 0xFFu); }
-
-__device__ __forceinline__ void few_bar() {   // the consumer warps
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
+// Order this thread's shared-memory writes before later asynchronous-proxy reads (tcgen05.cp).
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void few_bar() {   // the epilogue warps
+  asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
 template <int MODE, int ACT>
 __global__ void __launch_bounds__(kFewThreads, 1)
-    few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ CUtensorMap tmW) {
+    few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ CUtensorMap tmW,
+               const __grid_constant__ CUtensorMap tmX) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const FewSmem L = few_smem(MODE, a.T, a.k, a.K, a.stages);
+  const FewSmem L = few_smem(MODE, a.T, a.k, a.k_tiles, a.stages);
   uint64_t* full_bar = (uint64_t*)(smem + L.ctrl);
   uint64_t* empty_bar = full_bar + kFewMaxStages;
-  volatile int* abort_flag = (volatile int*)(empty_bar + kFewMaxStages);
-  volatile int* s_last = abort_flag + 1;
-  int* s_fills = (int*)(abort_flag + 2);
-  int* s_used = (int*)(abort_flag + 3);
-  // tables of the routed modes
-  uint32_t* bitmap = (uint32_t*)(smem + L.tab);             // experts some token uses
-  int* prefix = (int*)(bitmap + 128);                       // used experts before each word
-  int* elist = prefix + 128;                                // the used experts, ascending
+  uint64_t* sf_full = empty_bar + kFewMaxStages;
+  uint64_t* acc_full = sf_full + kFewMaxStages;   // [2]
+  uint64_t* acc_empty = acc_full + 2;             // [2]
+  uint64_t* drain_bar = acc_empty + 2;
+  uint64_t* drain_sf = drain_bar + 1;
+  uint32_t* tmem_holder = (uint32_t*)(drain_sf + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_holder + 1);
+  int* fills = (int*)(tmem_holder + 2);           // [4]: weight producer, token producer, scale warp, MMA
+  volatile int* s_last = fills + 4;
+  int* s_used = fills + 5;
+  // experts in use
   const int slots = a.T * a.k;
-  int* s_idx = elist + slots;
+  uint32_t* bitmap = (uint32_t*)(smem + L.tab);
+  int* prefix = (int*)(bitmap + 128);             // used experts before each word
+  int* elist = prefix + 128;                      // the used experts, ascending
+  int* tokens = elist + slots;                    // [used expert]: a bit for each token that uses it
+  int* s_idx = tokens + slots;
   float* s_w = (float*)(s_idx + slots);
-  int* hrow = (int*)(s_w + slots);                          // [used expert][8]: the token's first slot j with it, or none
-  float* hw = (float*)(hrow + slots * kFewRows);            // [used expert][8]: its routing weight
-  float* red = (float*)(smem + L.red);
+  float* hw = s_w + slots;                        // [used expert][T]: the token's routing weight
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(smem_u32(full_bar + s), 1);
-      mbar_init(smem_u32(empty_bar + s), kFewWarps);
+      mbar_init(smem_u32(full_bar + s), 3);                          // two producers, the scale warp's commit
+      mbar_init(smem_u32(empty_bar + s), 1);
+      mbar_init(smem_u32(sf_full + s), MODE == FEW_DOWN ? 2 : 1);    // weight scales, and h's
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(acc_full + b), 1);
+      mbar_init(smem_u32(acc_empty + b), 8);
+    }
+    mbar_init(smem_u32(drain_bar), 1);
+    mbar_init(smem_u32(drain_sf), 1);
     *abort_flag = 0;
-    *s_fills = 0;
+    for (int r = 0; r < 4; ++r) fills[r] = 0;
     fence_mbar_init();
     prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
   }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), kFewTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
   griddep_wait();
   griddep_launch_dependents();
 
   int used = 1;
   if constexpr (MODE != FEW_LINEAR) {
-    const int n = slots;
     for (int i = tid; i < 128; i += kFewThreads) bitmap[i] = 0;
-    for (int i = tid; i < slots * kFewRows; i += kFewThreads) { hrow[i] = kNoSlot; hw[i] = 0.0f; }
+    for (int i = tid; i < slots; i += kFewThreads) tokens[i] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kFewThreads) {
+    for (int i = tid; i < slots; i += kFewThreads) {
       const int e = a.idx[i];
       s_idx[i] = e;
       if (MODE == FEW_DOWN) s_w[i] = a.w[i];
@@ -206,215 +183,263 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     __syncthreads();
     used = *s_used;
-    for (int i = tid; i < n; i += kFewThreads) {
-      const int e = s_idx[i];
+    for (int i = tid; i < slots; i += kFewThreads) {
+      const int e = s_idx[i], t = i / a.k;
       if (e < 0 || e >= a.E) continue;
       const int u = prefix[e >> 5] + __popc(bitmap[e >> 5] & ((1u << (e & 31)) - 1u));
       elist[u] = e;
-      atomicMin(&hrow[u * kFewRows + i / a.k], i % a.k);
+      atomicOr(&tokens[u], 1 << t);
+      if constexpr (MODE == FEW_DOWN) {
+        // an expert that a token names twice counts with the sum of both weights, in slot order
+        float w = 0.0f;
+        for (int j = 0; j < a.k; ++j)
+          if (s_idx[t * a.k + j] == e) w += s_w[t * a.k + j];
+        hw[u * a.T + t] = w;
+      }
     }
     __syncthreads();
-    if constexpr (MODE == FEW_DOWN) {
-      for (int i = tid; i < used * kFewRows; i += kFewThreads) {
-        const int j0 = hrow[i];
-        if (j0 == kNoSlot) continue;
-        const int t = i % kFewRows, e = elist[i / kFewRows];
-        float w = 0.0f;   // an expert named twice by a token counts with both weights
-        for (int j = j0; j < a.k; ++j)
-          if (s_idx[t * a.k + j] == e) w += s_w[t * a.k + j];
-        hw[i] = w;
-      }
-    }
   }
-  if constexpr (MODE != FEW_DOWN) {
-    // x resident: codes [T][K + 32], scales as floats [K / 32][8]
-    const int nb = a.K >> 5;
-    float* sx = (float*)(smem + L.sx);
-    for (int i = tid; i < kFewRows * nb; i += kFewThreads) {
-      const int t = i % kFewRows, b = i / kFewRows;
-      float sc = 0.0f;
-      if (t < a.T) {
-        uint32_t code[8];
-        if (a.x) {
-          const uint4* src = (const uint4*)(a.x + (size_t)t * a.K + b * 32);
-          uint4 in[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) in[q] = src[q];
-          sc = e8m0_f32(quant_block_e4m3(in, code));
-        } else {
-          const uint4* src = (const uint4*)(a.xq + (size_t)t * a.K + b * 32);
-          const uint4 lo = src[0], hi = src[1];
-          code[0] = lo.x; code[1] = lo.y; code[2] = lo.z; code[3] = lo.w;
-          code[4] = hi.x; code[5] = hi.y; code[6] = hi.z; code[7] = hi.w;
-          sc = e8m0_f32(a.xs[(size_t)t * nb + b]);
-        }
-        uint4* dst = (uint4*)(smem + L.x + t * (a.K + 32) + b * 32);
-        dst[0] = make_uint4(code[0], code[1], code[2], code[3]);
-        dst[1] = make_uint4(code[4], code[5], code[6], code[7]);
-      }
-      sx[b * kFewRows + t] = sc;
-    }
-  }
-  __syncthreads();
 
-  // this CTA's steps
+  // this CTA's steps [s0, s1) of tiles x KT
   const int tiles = MODE == FEW_GLU ? used * a.m_tiles : a.m_tiles;
   const int KT = MODE == FEW_DOWN ? used * a.k_tiles : a.k_tiles;
   const long long total = (long long)tiles * KT;
   const long long G = total < (long long)gridDim.x ? total : (long long)gridDim.x;
   const int c = blockIdx.x;
   const int s0 = c < G ? (int)(c * total / G) : 0, s1 = c < G ? (int)((c + 1) * total / G) : 0;
+  // A run: consecutive steps of one matrix and one tile, accumulated in TMEM.  [kb, kb + n) are its K
+  // tiles, kk the first one's place in the tile's contraction.
+  struct Run { int tile, u, m, kk, kb, n; };
+  auto run_at = [&](int s) {
+    Run r;
+    r.tile = s / KT;
+    r.kk = s - r.tile * KT;
+    r.u = MODE == FEW_GLU ? r.tile / a.m_tiles : MODE == FEW_DOWN ? r.kk / a.k_tiles : 0;
+    r.m = MODE == FEW_GLU ? r.tile - r.u * a.m_tiles : r.tile;
+    r.kb = MODE == FEW_DOWN ? r.kk - r.u * a.k_tiles : r.kk;
+    r.n = min(a.k_tiles - r.kb, s1 - s);
+    return r;
+  };
 
-  if (warp == kFewWarps) {
-    // ------------------------------------------------------------- producer
-    const uint64_t pol = policy_evict_first();
-    int stage = 0, fills = 0;
-    uint32_t phase = 0;
-    int tile = KT ? s0 / KT : 0, kk = KT ? s0 % KT : 0;
-    for (int s = s0; s < s1; ++s) {
-      int ok = 1;
-      if (lane == 0) ok = mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, a.status, abort_flag);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      int u = 0, m = tile, kt = kk;
-      if (MODE == FEW_GLU) { u = tile / a.m_tiles; m = tile % a.m_tiles; }
-      if (MODE == FEW_DOWN) { u = kk / a.k_tiles; kt = kk % a.k_tiles; }
-      const int e = MODE == FEW_LINEAR ? 0 : elist[u];
-      const size_t blk = ((size_t)e * a.m_tiles + m) * a.k_tiles + kt;
-      const uint32_t bar = smem_u32(full_bar + stage);
-      int j = kNoSlot;
-      int nh = 0;
-      if constexpr (MODE == FEW_DOWN) {
-        if (lane < kFewRows) j = hrow[u * kFewRows + lane];
-        nh = __popc(__ballot_sync(0xffffffffu, j != kNoSlot));
-      }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, kFewTile + 1024 + nh * kFewHRow);
-        tma_load_2d(smem_u32(smem + stage * kFewTile), &tmW, bar, 0, (int)(blk * 256), pol);
-        bulk_load(smem_u32(smem + L.sf + stage * 1024), a.sf + blk * 1024, 1024, bar);
-      }
-      __syncwarp();
-      if constexpr (MODE == FEW_DOWN) {
-        if (j != kNoSlot)
-          bulk_load(smem_u32(smem + L.xst + (stage * kFewRows + lane) * kFewHStride),
-                    a.himg + ((size_t)(lane * a.k + j) * a.k_tiles + kt) * kFewHRow, kFewHRow, bar);
-      }
-      ++fills;
-      if (++kk == KT) { kk = 0; ++tile; }
-      if (++stage == a.stages) { stage = 0; phase ^= 1; }
-    }
-    if (lane == 0) *s_fills = fills;
-  } else {
-    // ------------------------------------------------------------- consumers
-    const int g = lane >> 2, q = lane & 3, half = warp >> 3, wr = (warp & 7) * 16;
-    const uint32_t row_off = (uint32_t)(wr + g) * 64 + q * 4;
-    const uint32_t sw_off = (uint32_t)(((wr + g) & 31) * 16 + ((wr + g) >> 5) * 4);
-    const uint32_t sw_off8 = (uint32_t)(((wr + g + 8) & 31) * 16 + ((wr + g + 8) >> 5) * 4);
-    const uint32_t swz = (uint32_t)((g >> 1) & 3);
-    int stage = 0;
-    uint32_t phase = 0;
-    int tile = KT ? s0 / KT : 0;
-    int s = s0;
-    while (s < s1) {
-      const int kb = s - tile * KT;                       // this segment: K steps [kb, ke) of the tile
-      const int ke = min(KT, kb + (s1 - s));
-      float acc[2][4] = {};
-      int u = 0, kt = kb;
-      if (MODE == FEW_DOWN) { u = kb / a.k_tiles; kt = kb % a.k_tiles; }
-      for (int kk = kb; kk < ke; ++kk) {
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(smem_u32(full_bar + stage), phase, a.status, abort_flag);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok) {
-          const uint32_t sW = smem_u32(smem + stage * kFewTile), sS = smem_u32(smem + L.sf + stage * 1024);
-          uint32_t sw[2][2];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            sw[m][0] = lds32(sS + m * 512 + sw_off);
-            sw[m][1] = lds32(sS + m * 512 + sw_off8);
-          }
-          uint32_t xrow = 0, xsc[2] = {0, 0};
-          bool have;
-          float w2[2] = {1.0f, 1.0f};
-          if constexpr (MODE == FEW_DOWN) {
-            const uint32_t st = smem_u32(smem + L.xst + stage * kFewRows * kFewHStride);
-            have = hrow[u * kFewRows + g] != kNoSlot;
-            xrow = st + g * kFewHStride;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int t = 2 * q + i;
-              // a token that does not use the expert: its columns are zeros, its scale a finite one
-              xsc[i] = hrow[u * kFewRows + t] != kNoSlot ? lds32(st + t * kFewHStride + 128) : 0u;
-              w2[i] = hw[u * kFewRows + t];
-            }
-          } else {
-            have = g < a.T;
-            xrow = smem_u32(smem + L.x) + g * (a.K + 32) + kt * 128;
-          }
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int j = 2 * half + jj;
-            const uint2 xv = have ? lds64(xrow + 32 * j + 8 * q) : make_uint2(0u, 0u);
-            uint32_t b[4];
-            e4m3x8_to_f16(xv, b);
-            float sx[2];
-            if constexpr (MODE == FEW_DOWN) {
-              sx[0] = e8m0_byte_f32(xsc[0], j) * w2[0];
-              sx[1] = e8m0_byte_f32(xsc[1], j) * w2[1];
-            } else {
-              const uint2 v = lds64(smem_u32(smem + L.sx) + ((kt * 4 + j) * kFewRows + 2 * q) * 4);
-              sx[0] = __uint_as_float(v.x);
-              sx[1] = __uint_as_float(v.y);
-            }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const uint32_t addr = sW + m * 8192 + row_off + ((j ^ swz) << 4);
-              uint32_t lo[4], hi[4];
-              e2m1x8_to_f16(lds32(addr), lo);
-              e2m1x8_to_f16(lds32(addr + 512), hi);
-              float p[4] = {};
-              mma_f16(p, lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
-              mma_f16(p, lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
-              const float r0 = e8m0_byte_f32(sw[m][0], j), r1 = e8m0_byte_f32(sw[m][1], j);
-              acc[m][0] = fmaf(p[0], r0 * sx[0], acc[m][0]);
-              acc[m][1] = fmaf(p[1], r0 * sx[1], acc[m][1]);
-              acc[m][2] = fmaf(p[2], r1 * sx[0], acc[m][2]);
-              acc[m][3] = fmaf(p[3], r1 * sx[1], acc[m][3]);
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(empty_bar + stage));
+  if (warp == 0) {
+    // ------------------------------------------------------------- producer: weights
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_first();
+      int stage = 0, nfill = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int s = s0; s < s1 && ok;) {
+        const Run r = run_at(s);
+        const int e = MODE == FEW_LINEAR ? 0 : elist[r.u];
+        const size_t blk = ((size_t)e * a.m_tiles + r.m) * a.k_tiles + r.kb;
+        for (int i = 0; i < r.n; ++i) {
+          ok = mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, a.status, abort_flag);
+          if (!ok) break;
+          const uint32_t sb = smem_u32(sf_full + stage), fb = smem_u32(full_bar + stage);
+          mbar_arrive_expect_tx(sb, 1024);
+          bulk_load(smem_u32(smem + L.sf + stage * kFewSF), a.sf + (blk + i) * 1024, 1024, sb);
+          mbar_arrive_expect_tx(fb, kFewTile);
+          tma_load_2d(smem_u32(smem + stage * kFewStage), &tmW, fb, 0, (int)((blk + i) * 256), pol);
+          ++nfill;
+          if (++stage == a.stages) { stage = 0; phase ^= 1; }
         }
-        if (MODE == FEW_DOWN && ++kt == a.k_tiles) { kt = 0; ++u; }
-        if (MODE != FEW_DOWN) ++kt;
+        s += r.n;
+      }
+      fills[0] = nfill;
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------- producer: token rows
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();
+      int stage = 0, nfill = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int s = s0; s < s1 && ok;) {
+        const Run r = run_at(s);
+        for (int i = 0; i < r.n; ++i) {
+          ok = mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, a.status, abort_flag);
+          if (!ok) break;
+          const uint32_t fb = smem_u32(full_bar + stage);
+          if constexpr (MODE == FEW_DOWN) {
+            const uint32_t sb = smem_u32(sf_full + stage);
+            mbar_arrive_expect_tx(sb, 512);
+            bulk_load(smem_u32(smem + L.sf + stage * kFewSF + 1024), a.hs + ((size_t)r.u * a.k_tiles + r.kb + i) * 512, 512, sb);
+          }
+          mbar_arrive_expect_tx(fb, kFewBTile);
+          // rows past the operand's tokens are another expert's, or zeros behind the tensor's end:
+          // they reach accumulator columns that nothing reads
+          tma_load_2d(smem_u32(smem + stage * kFewStage + kFewATile), &tmX, fb, (r.kb + i) * 128,
+                      MODE == FEW_DOWN ? r.u * a.T : 0, pol);
+          ++nfill;
+          if (++stage == a.stages) { stage = 0; phase ^= 1; }
+        }
+        s += r.n;
+      }
+      fills[1] = nfill;
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------- scale factors -> TMEM
+    uint32_t* xs = (uint32_t*)(smem + L.xs);
+    if constexpr (MODE != FEW_DOWN) {
+      for (int i = lane; i < a.T * a.k_tiles; i += 32) xs[i] = ((const uint32_t*)a.xs)[i];
+      __syncwarp();
+    }
+    const uint64_t sf_desc0 = smem_desc(smem_u32(smem + L.sf), 16, 128, 0);
+    int stage = 0, nfill = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int s = s0; s < s1 && ok;) {
+      const Run r = run_at(s);
+      for (int i = 0; i < r.n; ++i) {
+        int got = 1;
+        if (lane == 0) got = mbar_wait(smem_u32(sf_full + stage), phase, a.status, abort_flag);
+        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+        if (!ok) break;
+        if constexpr (MODE != FEW_DOWN) {
+          // the token scales' atom: row t's four bytes at 16 t (its last reader, the copy of the
+          // stage's previous round, finished before the stage was released)
+          if (lane < kFewRows)
+            *(uint32_t*)(smem + L.sf + stage * kFewSF + 1024 + 16 * lane) = lane < a.T ? xs[lane * a.k_tiles + r.kb + i] : 0u;
+          fence_async_shared();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t desc = sf_desc0 + (uint64_t)((stage * kFewSF) >> 4);
+          const uint32_t tsf = tmem_base + 64 + 16 * stage;
+          tc_cp_32x128b_warpx4(tsf, desc);
+          tc_cp_32x128b_warpx4(tsf + 4, desc + (uint64_t)(512 >> 4));
+          tc_cp_32x128b_warpx4(tsf + 8, desc + (uint64_t)(1024 >> 4));
+          tc_commit(smem_u32(full_bar + stage));
+        }
+        __syncwarp();
+        ++nfill;
         if (++stage == a.stages) { stage = 0; phase ^= 1; }
       }
-      // ---- the segment's sums: red[t][row]
-      few_bar();   // the previous segment's readers are done
-      if (half == 1) {
+      s += r.n;
+    }
+    if (lane == 0) {
+      tc_commit(smem_u32(drain_sf));   // every copy lands before TMEM is released
+      mbar_wait_drain(smem_u32(drain_sf), 0);
+      fills[2] = nfill;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, 2);
+      uint32_t idesc[4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+      for (int j = 0; j < 4; ++j) idesc[j] = idesc_mx_e2m1_e4m3(128, kFewRows, j, j);
+      int stage = 0, nfill = 0, nrun = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int s = s0; s < s1 && ok;) {
+        const Run r = run_at(s);
+        const int abuf = nrun & 1;
+        const uint32_t acc_t = tmem_base + 32 * abuf;
+        auto issue_stage = [&](int st, uint32_t acc0) {
+          const uint64_t a_desc = desc0 + (uint64_t)((st * kFewStage) >> 4);
+          const uint64_t b_desc = a_desc + (uint64_t)(kFewATile >> 4);
+          const uint32_t tsf = tmem_base + 64 + 16 * st;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) red[(2 * q + (i & 1)) * kFewRedStride + m * 128 + wr + g + 8 * (i >> 1)] = acc[m][i];
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_mxf8f6f4(acc_t + h * kFewRows, a_desc + (uint64_t)((h * 16384 + 32 * j) >> 4),
+                           b_desc + (uint64_t)((32 * j) >> 4), idesc[j], (tsf + 4 * h) | ((uint32_t)j << 30),
+                           (tsf + 8) | ((uint32_t)j << 30), j > 0 ? 1u : acc0);
+        };
+        // the accumulator is free once the epilogue has drained the run before the last one
+        ok = mbar_wait(smem_u32(acc_empty + abuf), (uint32_t)(nrun >> 1 & 1) ^ 1u, a.status, abort_flag);
+        if (!ok) break;
+        for (int i = 0; i < r.n;) {
+          const int stage2 = stage + 1 == a.stages ? 0 : stage + 1;
+          const uint32_t phase2 = stage + 1 == a.stages ? phase ^ 1u : phase;
+          ok = mbar_wait(smem_u32(full_bar + stage), phase, a.status, abort_flag);
+          if (!ok) break;
+          // a second stage in the same round where it has landed already
+          const bool two = i + 1 < r.n && mbar_try_wait(smem_u32(full_bar + stage2), phase2);
+          tc_fence_after();
+          issue_stage(stage, i > 0 ? 1u : 0u);
+          tc_commit(smem_u32(empty_bar + stage));
+          if (two) {
+            issue_stage(stage2, 1u);
+            tc_commit(smem_u32(empty_bar + stage2));
+          }
+          i += two ? 2 : 1;
+          nfill += two ? 2 : 1;
+          stage = stage2;
+          phase = phase2;
+          if (two && ++stage == a.stages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        tc_commit(smem_u32(acc_full + abuf));
+        ++nrun;
+        s += r.n;
       }
-      few_bar();
-      if (half == 0) {
+      tc_commit(smem_u32(drain_bar));   // every MMA has finished before TMEM is released
+      mbar_wait_drain(smem_u32(drain_bar), 0);
+      fills[3] = nfill;
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- epilogue: a thread per weight row
+    // (a wait that gives up does not leave the loop: all eight warps meet at the same barriers)
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int row = half * 128 + q * 32 + lane;
+    const int et = tid - 64;   // 0 .. 255
+    float* red = (float*)(smem + L.red);
+    int nrun = 0;
+    for (int s = s0; s < s1;) {
+      // a segment: this CTA's runs of one tile
+      float acc[kFewRows];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+      for (int t = 0; t < kFewRows; ++t) acc[t] = 0.0f;
+      const Run first = run_at(s);
+      bool whole = false;
+      for (;;) {
+        const Run r = run_at(s);
+        const int abuf = nrun & 1;
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(smem_u32(acc_full + abuf), (uint32_t)(nrun >> 1 & 1), a.status, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        tc_fence_after();
+        uint32_t v[kFewRows];
+        tmem_ld16(tmem_base + 32 * abuf + half * kFewRows + ((uint32_t)(q * 32) << 16), v);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(smem_u32(acc_empty + abuf));
+        if constexpr (MODE == FEW_DOWN) {
+          const int have = tokens[r.u];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) red[(2 * q + (i & 1)) * kFewRedStride + m * 128 + wr + g + 8 * (i >> 1)] += acc[m][i];
+          for (int t = 0; t < kFewRows; ++t)
+            if (have >> t & 1) acc[t] = fmaf(hw[r.u * a.T + t], __uint_as_float(v[t]), acc[t]);
+        } else {
+#pragma unroll
+          for (int t = 0; t < kFewRows; ++t) acc[t] = __uint_as_float(v[t]);
+        }
+        ++nrun;
+        s += r.n;
+        whole = r.kk + r.n == KT;
+        if (whole || s == s1) break;
       }
-      few_bar();
+      const int tile = first.tile;
       bool finish = true;
-      if (kb != 0 || ke != KT) {
+      if (first.kk != 0 || !whole) {
         // part of the tile's contraction: publish it; the last of the tile's CTAs adds them up
-        float* mine = a.part + (size_t)(2 * c + (kb == 0 ? 1 : 0)) * kFewPart;
-        for (int i = tid; i < a.T * 256; i += 32 * kFewWarps) mine[i] = red[(i >> 8) * kFewRedStride + (i & 255)];
+        float* mine = a.part + (size_t)(2 * c + (first.kk == 0 ? 1 : 0)) * kFewPart + row;
+#pragma unroll
+        for (int t = 0; t < kFewRows; ++t)
+          if (t < a.T) mine[t * 256] = acc[t];
         __threadfence();
         few_bar();
         const long long t0 = (long long)tile * KT;
         const int c_lo = (int)(((t0 + 1) * G - 1) / total), c_hi = (int)(((t0 + KT) * G - 1) / total);
-        if (tid == 0) {
+        if (et == 0) {
           const bool last = atomicAdd(a.counters + c_lo, 1u) == (unsigned)(c_hi - c_lo);
           if (last) a.counters[c_lo] = 0;
           __threadfence();
@@ -423,55 +448,74 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         few_bar();
         finish = *s_last;
         if (finish) {
-          for (int i = tid; i < a.T * 256; i += 32 * kFewWarps) {
-            float v = __ldcg(a.part + (size_t)(2 * c_lo + 1) * kFewPart + i);
-            for (int p = c_lo + 1; p <= c_hi; ++p) v += __ldcg(a.part + (size_t)(2 * p) * kFewPart + i);
-            red[(i >> 8) * kFewRedStride + (i & 255)] = v;
+          const float* p = a.part + (size_t)(2 * c_lo + 1) * kFewPart + row;
+#pragma unroll
+          for (int t = 0; t < kFewRows; ++t) acc[t] = t < a.T ? __ldcg(p + t * 256) : 0.0f;
+          for (int i = c_lo + 1; i <= c_hi; ++i) {
+            p = a.part + (size_t)(2 * i) * kFewPart + row;
+#pragma unroll
+            for (int t = 0; t < kFewRows; ++t)
+              if (t < a.T) acc[t] += __ldcg(p + t * 256);
           }
-          few_bar();
         }
       }
       if (finish) {
         if constexpr (MODE == FEW_GLU) {
-          // a warp per (token, 32-channel block): glu, then the block's MX codes and scale
-          const int ux = tile / a.m_tiles, m = tile % a.m_tiles;
-          for (int i = warp; i < a.T * 4; i += kFewWarps) {
-            const int t = i >> 2, b = i & 3, j = hrow[ux * kFewRows + t];
-            if (j == kNoSlot) continue;
-            const float v = glu_f<ACT>(red[t * kFewRedStride + 32 * b + lane], red[t * kFewRedStride + 128 + 32 * b + lane]);
-            const uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
-            const int e = mx_exp_e4m3(amax);
-            uint8_t* dst = a.himg + ((size_t)(t * a.k + j) * a.m_tiles + m) * kFewHRow;
-            dst[32 * b + lane] = (uint8_t)(f32x2_to_e4m3x2(v * __uint_as_float((uint32_t)(127 - e) << 23), 0.0f) & 0xFFu);
-            if (lane == 0) dst[128 + b] = (uint8_t)(e + 127);
+          // the up half hands its values to the gate half, whose warps hold one 32-channel block each
+          const int ch = row & 127;
+          few_bar();
+          if (half == 1) {
+#pragma unroll
+            for (int t = 0; t < kFewRows; ++t)
+              if (t < a.T) red[t * 128 + ch] = acc[t];
+          }
+          few_bar();
+          if (half == 0) {
+            const int have = tokens[first.u];
+            uint8_t* codes = a.hq + (size_t)first.u * a.T * a.m_tiles * 128 + first.m * 128 + ch;
+            uint8_t* atom = a.hs + ((size_t)first.u * a.m_tiles + first.m) * 512 + q;
+#pragma unroll
+            for (int t = 0; t < kFewRows; ++t) {
+              if (!(have >> t & 1)) continue;
+              const float h = glu_f<ACT>(acc[t], red[t * 128 + ch]);
+              const int e = mx_exp_e4m3(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu));
+              const float v = h * __uint_as_float((uint32_t)(127 - e) << 23);
+              codes[(size_t)t * a.m_tiles * 128] = (uint8_t)(f32x2_to_e4m3x2(v, 0.0f) & 0xFFu);
+              if (lane == 0) atom[16 * t] = (uint8_t)(e + 127);
+            }
           }
         } else {
-          for (int i = tid; i < a.T * 256; i += 32 * kFewWarps) {
-            const int t = i >> 8, r = i & 255, row = tile * 256 + r;
-            if (row >= a.rows) continue;
-            const size_t o = (size_t)t * a.rows + row;
-            float v = red[t * kFewRedStride + r];
-            if (MODE == FEW_DOWN && a.ys) v += a.ys[o];
-            if (MODE == FEW_LINEAR && a.y_f32) ((float*)a.y)[o] = v;
-            else ((__nv_bfloat16*)a.y)[o] = __float2bfloat16_rn(v);
+          const int o_row = tile * 256 + row;
+          if (o_row < a.rows) {
+#pragma unroll
+            for (int t = 0; t < kFewRows; ++t) {
+              if (t >= a.T) break;
+              const size_t o = (size_t)t * a.rows + o_row;
+              if (MODE == FEW_LINEAR && a.y_f32) ((float*)a.y)[o] = acc[t];
+              else ((__nv_bfloat16*)a.y)[o] = __float2bfloat16_rn(acc[t] + (MODE == FEW_DOWN && a.ys ? a.ys[o] : 0.0f));
+            }
           }
         }
       }
-      s += ke - kb;
-      ++tile;
     }
     if (MODE == FEW_DOWN && total == 0) {
       // every id was invalid: the shared expert's output alone
-      for (size_t i = (size_t)c * 32 * kFewWarps + tid; i < (size_t)a.T * a.rows; i += (size_t)gridDim.x * 32 * kFewWarps)
+      for (size_t i = (size_t)c * 256 + et; i < (size_t)a.T * a.rows; i += (size_t)gridDim.x * 256)
         ((__nv_bfloat16*)a.y)[i] = __float2bfloat16_rn(a.ys ? a.ys[i] : 0.0f);
     }
   }
   __syncthreads();
-  if (*abort_flag && tid == 0) {
+  if (*abort_flag) {
     // a wait gave up: let the copies still in flight land before the CTA's shared memory is released
-    const int f1 = *s_fills;
-    for (int f = max(0, f1 - a.stages); f < f1; ++f)
-      mbar_wait_drain(smem_u32(full_bar + f % a.stages), (uint32_t)(f / a.stages) & 1u);
+    if (tid == 0) {
+      drain_ring(full_bar, a.stages, fills, 3, fills[3]);
+      drain_ring(sf_full, a.stages, fills, MODE == FEW_DOWN ? 2 : 1, fills[2]);
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kFewTmemCols);
   }
 }
 

@@ -281,7 +281,7 @@ moe_status_t moe_add_rmsnorm_mxfp8(const void* x_bf16, const void* residual, moe
 
 /* ---- MXFP4 linear --------------------------------------------------------------------------
  * y[t] = W x[t] for a weight matrix W [N][K] in MXFP4 and rows x in MXFP8 (both with one E8M0
- * scale per 32 elements along K, accumulation in fp32).  Up to 8 rows (and T K <= 80 KB) run as
+ * scale per 32 elements along K, accumulation in fp32).  Up to 16 rows run as
  * a stream of the weights over all SMs, more rows on the tensor cores' block-scaled GEMM; both
  * read the same packed weights.
  * moe_linear_create: a host object for calls of up to T_max rows on matrices of one shape;
@@ -310,7 +310,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t linear, const uint8_t* q_e4m3, const 
                               const moe_matrix_mxfp4* weights, void* y, moe_type_t y_type, void* stream);
 
 /* ---- the layer for a few tokens -------------------------------------------------------------
- * moe_forward's layer for 1 <= T <= 8 tokens of a decode step, from the same packed experts: the
+ * moe_forward's layer for 1 <= T <= 16 tokens of a decode step, from the same packed experts: the
  * gate/up and down products stream the touched experts' weights once, split evenly over the SMs,
  * instead of running one tile per expert.  The same roundings as moe_forward except that the
  * experts' outputs are summed in fp32 (moe_forward holds each in bf16).
@@ -319,7 +319,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t linear, const uint8_t* q_e4m3, const 
  * [T][d/32], the MXFP8 form of the tokens (moe_add_rmsnorm_mxfp8, moe_quant_mxfp8), or both NULL.
  * Other arguments as moe_forward.  An id outside [0, E) contributes nothing and is flagged
  * (MOE_ERR_DEVICE_FAULT at moe_plan_check); an expert that a token names twice counts with the
- * sum of both weights.  T <= 8, T d <= 80 KB; not for latent plans (MOE_ERR_INVALID_ARG).  Uses the
+ * sum of both weights.  T <= 16; not for latent plans (MOE_ERR_INVALID_ARG).  Uses the
  * plan workspace (one call at a time per plan). */
 moe_status_t moe_forward_decode(moe_plan_t plan, const void* x_bf16, const uint8_t* q_e4m3,
                                 const uint8_t* scale_e8m0, int T, const int32_t* idx, const float* w,

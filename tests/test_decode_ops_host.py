@@ -93,7 +93,6 @@ def test_forward_decode_refusals():
     L = api.lib()
     h = api.moe_plan_create(64, 256, 8, 2, 128)
     hs = api.moe_plan_create(64, 256, 8, 2, 128, 128)
-    wide = api.moe_plan_create(64, 16384, 8, 2, 128)
     lat = api.moe_plan_create(64, 256, 8, 2, 128)
     assert L.moe_plan_set_latent(lat, 128, ctypes.c_float(1e-5)) == 0
     ex, sh = api.ExpertsMXFP4(*[A.value] * 4), api.SharedBF16(A.value, A.value)
@@ -103,7 +102,7 @@ def test_forward_decode_refusals():
         return L.moe_forward_decode(h, x, q, s, T, idx, w, ref(ex), ref(sh), y, None)
 
     assert call(h=None) == INVALID and call(h=lat) == INVALID
-    assert call(T=-1) == INVALID and call(T=9) == SHAPE and call(h=wide, T=8) == SHAPE
+    assert call(T=-1) == INVALID and call(T=17) == SHAPE
     assert call(x=None) == INVALID                                    # neither form of the tokens
     assert call(q=A) == INVALID and call(s=A) == INVALID              # codes and scales come together
     assert call(idx=None) == INVALID and call(w=None) == INVALID and call(y=None) == INVALID and call(ex=None) == INVALID
@@ -116,7 +115,7 @@ def test_forward_decode_refusals():
     assert call(ex=api.ExpertsMXFP4(A.value + 16, A.value, A.value, A.value)) == ALIGN
     assert call() == NOT_INIT and call(x=None, q=A, s=A) == NOT_INIT and call(h=hs, sh=sh) == NOT_INIT
     assert call(T=0) == 0
-    for p in (h, hs, wide, lat):
+    for p in (h, hs, lat):
         api.moe_plan_destroy(p)
 
 

@@ -146,7 +146,7 @@ def check_linear(q, s, w, y, rows=None):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T, N, K", [(1, 1, 128), (1, 256, 128), (2, 257, 256), (3, 255, 640), (5, 1003, 640), (8, 512, 1152),
-                                     (7, 40, 7168), (4, 3333, 384), (8, 300, 10240), (8, 130, 10368), (6, 260, 20480),
+                                     (7, 40, 7168), (4, 3333, 384), (8, 300, 10240), (8, 130, 10368), (6, 260, 20480), (16, 1003, 896), (13, 513, 512), (17, 300, 640),
                                      (9, 1003, 640), (64, 257, 256), (65, 7, 1152), (300, 512, 2048), (177, 1000, 128)])
 def test_linear(T, N, K, dtype):
     q, s, lin, w = linear_case(T, N, K, T * 1000 + N)
@@ -255,7 +255,8 @@ def draws(T, E, k, seed):
 @pytest.mark.parametrize("T, d, E, k, I, Is, act", [
     (1, 128, 1, 1, 128, 0, "silu"), (1, 256, 16, 4, 128, 128, "silu"), (2, 384, 8, 3, 256, 0, "clamped_swiglu"),
     (3, 512, 32, 4, 256, 0, "silu"), (5, 1152, 10, 3, 640, 384, "silu"), (8, 256, 40, 32, 128, 0, "silu"),
-    (8, 640, 4, 4, 384, 256, "clamped_swiglu"), (7, 256, 300, 8, 128, 0, "silu"), (8, 1024, 64, 16, 512, 0, "silu")])
+    (8, 640, 4, 4, 384, 256, "clamped_swiglu"), (7, 256, 300, 8, 128, 0, "silu"), (8, 1024, 64, 16, 512, 0, "silu"),
+    (16, 384, 64, 32, 256, 128, "silu"), (11, 256, 4096, 2, 128, 0, "silu")])
 def test_forward_decode(T, d, E, k, I, Is, act):
     case = Case(synth.custom(seed=T + E, T=T, d=d, E=E, k=k, I=I, I_shared=Is), act=act)
     idx, w = draws(T, E, k, 5)
