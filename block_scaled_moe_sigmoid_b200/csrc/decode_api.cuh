@@ -200,7 +200,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
     a.part = p->at<float>(p->o_part);
     a.counters = p->at<unsigned int>(p->o_cnt);
     a.status = p->at<unsigned int>(p->o_status);
-    const int grid = (int)std::min<long long>((long long)m_tiles * k_tiles, std::min(p->num_sms, kFewMaxCtas));
+    const int grid = std::min(m_tiles * k_tiles, std::min(p->num_sms, kFewMaxCtas));
     return launch_few<FEW_LINEAR, 0>(a, tW, tX, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   // more rows: the block-scaled GEMM on one dense group

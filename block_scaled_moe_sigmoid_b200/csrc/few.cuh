@@ -23,9 +23,10 @@
 // products on mma.sync were measured too: making f16 operands out of the codes then takes more than
 // the load (40000 x 7168, 8 rows: cvt 3.0 TB/s, half of it by bit moves 2.6 TB/s, E4M3 operands 2.4 TB/s).
 //
-// Roles (384 threads): warp 0 loads weight tiles and their scales, warp 10 the token rows (a 16-row
-// box per step), warp 11 moves each step's scales into TMEM, warp 1 issues the MMAs, warps 2 to 9 run
-// the epilogue, a thread per weight row.
+// Roles (416 threads): warp 0 loads weight tiles and their scales, warp 10 the token rows (a 16-row
+// box per step), warp 11 moves each step's scales into TMEM, warps 1 and 12 issue the MMAs of one
+// 128-row half each (one thread forms and issues an instruction in about 90 cycles, and eight of them
+// would take longer than the step's load), warps 2 to 9 run the epilogue, a thread per weight row.
 #pragma once
 #include "gemm.cuh"
 #include "kernels.cuh"
@@ -34,7 +35,7 @@ namespace moe {
 
 enum { FEW_LINEAR = 0, FEW_GLU = 1, FEW_DOWN = 2 };
 constexpr int kFewRows = 16;                   // tokens per call: the MMA's N
-constexpr int kFewThreads = 384;
+constexpr int kFewThreads = 416;
 constexpr int kFewTile = 256 * 64;             // bytes of codes per step
 constexpr int kFewATile = 256 * 128;           // the same in shared memory, a byte per code
 constexpr int kFewBTile = kFewRows * 128;
@@ -91,6 +92,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 // Order this thread's shared-memory writes before later asynchronous-proxy reads (tcgen05.cp).
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Steps that stay together in a CTA: a whole tile, or one step.  Split tiles cost the exchange of
+// partials, about 3 us at the end of the call, the time of kFewSplitCost steps; whole tiles cost the
+// last wave's idle CTAs.
+constexpr int kFewSplitCost = 8;
+__host__ __device__ inline int few_unit(int tiles, int KT, int grid) {
+  const long long total = (long long)tiles * KT;
+  return (long long)((tiles + grid - 1) / grid) * KT <= (total + grid - 1) / grid + kFewSplitCost ? KT : 1;
+}
 __device__ __forceinline__ void few_bar() {   // the epilogue warps
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
@@ -111,9 +120,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   uint64_t* drain_sf = drain_bar + 1;
   uint32_t* tmem_holder = (uint32_t*)(drain_sf + 1);
   volatile int* abort_flag = (volatile int*)(tmem_holder + 1);
-  int* fills = (int*)(tmem_holder + 2);           // [4]: weight producer, token producer, scale warp, MMA
-  volatile int* s_last = fills + 4;
-  int* s_used = fills + 5;
+  int* fills = (int*)(tmem_holder + 2);           // [5]: weight producer, token producer, scale warp, MMA halves
+  volatile int* s_last = fills + 5;
+  int* s_used = fills + 6;
   // experts in use
   const int slots = a.T * a.k;
   uint32_t* bitmap = (uint32_t*)(smem + L.tab);
@@ -128,17 +137,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(smem_u32(full_bar + s), 3);                          // two producers, the scale warp's commit
-      mbar_init(smem_u32(empty_bar + s), 1);
+      mbar_init(smem_u32(empty_bar + s), 2);                         // both issuers
       mbar_init(smem_u32(sf_full + s), MODE == FEW_DOWN ? 2 : 1);    // weight scales, and h's
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(acc_full + b), 1);
+      mbar_init(smem_u32(acc_full + b), 2);
       mbar_init(smem_u32(acc_empty + b), 8);
     }
-    mbar_init(smem_u32(drain_bar), 1);
+    mbar_init(smem_u32(drain_bar), 2);
     mbar_init(smem_u32(drain_sf), 1);
     *abort_flag = 0;
-    for (int r = 0; r < 4; ++r) fills[r] = 0;
+    for (int r = 0; r < 5; ++r) fills[r] = 0;
     fence_mbar_init();
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmX);
@@ -151,7 +160,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  griddep_wait();
+  // FEW_DOWN always follows FEW_GLU, which lets it start only after its own wait: all that was
+  // launched before FEW_GLU is done by then, the ids, the routing weights and the packed weights
+  // among it.  So its tables and weight loads begin here, and what FEW_GLU writes, and every buffer
+  // that it shares with it, waits (token producer, epilogue).
+  if (MODE != FEW_DOWN) griddep_wait();
   griddep_launch_dependents();
 
   int used = 1;
@@ -203,10 +216,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   // this CTA's steps [s0, s1) of tiles x KT
   const int tiles = MODE == FEW_GLU ? used * a.m_tiles : a.m_tiles;
   const int KT = MODE == FEW_DOWN ? used * a.k_tiles : a.k_tiles;
-  const long long total = (long long)tiles * KT;
-  const long long G = total < (long long)gridDim.x ? total : (long long)gridDim.x;
+  const int total = tiles * KT;
+  const int unit = few_unit(tiles, KT, gridDim.x);      // a CTA's steps are whole units
+  const long long units = total / max(unit, 1);
+  const long long G = min(units, (long long)gridDim.x);
   const int c = blockIdx.x;
-  const int s0 = c < G ? (int)(c * total / G) : 0, s1 = c < G ? (int)((c + 1) * total / G) : 0;
+  const int s0 = c < G ? (int)(c * units / G) * unit : 0, s1 = c < G ? (int)((c + 1) * units / G) * unit : 0;
   // A run: consecutive steps of one matrix and one tile, accumulated in TMEM.  [kb, kb + n) are its K
   // tiles, kk the first one's place in the tile's contraction.
   struct Run { int tile, u, m, kk, kb, n; };
@@ -255,6 +270,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       int stage = 0, nfill = 0;
       uint32_t phase = 0;
       bool ok = true;
+      if (MODE == FEW_DOWN) griddep_wait();
       for (int s = s0; s < s1 && ok;) {
         const Run r = run_at(s);
         for (int i = 0; i < r.n; ++i) {
@@ -281,11 +297,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __syncwarp();
   } else if (warp == 11) {
     // ------------------------------------------------------------- scale factors -> TMEM
-    uint32_t* xs = (uint32_t*)(smem + L.xs);
-    if constexpr (MODE != FEW_DOWN) {
-      for (int i = lane; i < a.T * a.k_tiles; i += 32) xs[i] = ((const uint32_t*)a.xs)[i];
-      __syncwarp();
-    }
+    const uint32_t* xs = (const uint32_t*)(smem + L.xs);
+    if (MODE != FEW_DOWN) asm volatile("bar.sync 2, 288;" ::: "memory");   // the epilogue warps have loaded xs
     const uint64_t sf_desc0 = smem_desc(smem_u32(smem + L.sf), 16, 128, 0);
     int stage = 0, nfill = 0;
     uint32_t phase = 0;
@@ -326,9 +339,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       fills[2] = nfill;
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------- MMA issuer
+  } else if (warp == 1 || warp == 12) {
+    // ------------------------------------------------------------- MMA issuers, one per 128-row half
     if (lane == 0) {
+      const int h = warp == 12;
       const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, 2);
       uint32_t idesc[4];
 #pragma unroll
@@ -339,18 +353,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int s = s0; s < s1 && ok;) {
         const Run r = run_at(s);
         const int abuf = nrun & 1;
-        const uint32_t acc_t = tmem_base + 32 * abuf;
+        const uint32_t acc_t = tmem_base + 32 * abuf + kFewRows * h;
         auto issue_stage = [&](int st, uint32_t acc0) {
-          const uint64_t a_desc = desc0 + (uint64_t)((st * kFewStage) >> 4);
-          const uint64_t b_desc = a_desc + (uint64_t)(kFewATile >> 4);
+          const uint64_t a_desc = desc0 + (uint64_t)((st * kFewStage + h * 16384) >> 4);
+          const uint64_t b_desc = desc0 + (uint64_t)((st * kFewStage + kFewATile) >> 4);
           const uint32_t tsf = tmem_base + 64 + 16 * st;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              mma_mxf8f6f4(acc_t + h * kFewRows, a_desc + (uint64_t)((h * 16384 + 32 * j) >> 4),
-                           b_desc + (uint64_t)((32 * j) >> 4), idesc[j], (tsf + 4 * h) | ((uint32_t)j << 30),
-                           (tsf + 8) | ((uint32_t)j << 30), j > 0 ? 1u : acc0);
+            mma_mxf8f6f4(acc_t, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4), idesc[j],
+                         (tsf + 4 * h) | ((uint32_t)j << 30), (tsf + 8) | ((uint32_t)j << 30), j > 0 ? 1u : acc0);
         };
         // the accumulator is free once the epilogue has drained the run before the last one
         ok = mbar_wait(smem_u32(acc_empty + abuf), (uint32_t)(nrun >> 1 & 1) ^ 1u, a.status, abort_flag);
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       tc_commit(smem_u32(drain_bar));   // every MMA has finished before TMEM is released
       mbar_wait_drain(smem_u32(drain_bar), 0);
-      fills[3] = nfill;
+      fills[3 + h] = nfill;
     }
     __syncwarp();
   } else {
@@ -392,6 +403,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int row = half * 128 + q * 32 + lane;
     const int et = tid - 64;   // 0 .. 255
     float* red = (float*)(smem + L.red);
+    if constexpr (MODE == FEW_DOWN) {
+      griddep_wait();
+    } else {
+      uint32_t* xs = (uint32_t*)(smem + L.xs);
+      for (int i = et; i < a.T * a.k_tiles; i += 256) xs[i] = ((const uint32_t*)a.xs)[i];
+      asm volatile("bar.arrive 2, 288;" ::: "memory");
+    }
     int nrun = 0;
     for (int s = s0; s < s1;) {
       // a segment: this CTA's runs of one tile
@@ -435,11 +453,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
         for (int t = 0; t < kFewRows; ++t)
           if (t < a.T) mine[t * 256] = acc[t];
-        __threadfence();
         few_bar();
         const long long t0 = (long long)tile * KT;
-        const int c_lo = (int)(((t0 + 1) * G - 1) / total), c_hi = (int)(((t0 + KT) * G - 1) / total);
+        const int c_lo = (int)(((t0 + 1) * G - 1) / total), c_hi = (int)(((t0 + KT) * G - 1) / total);   // unit = 1
         if (et == 0) {
+          __threadfence();   // the CTA's partial, ordered before the count
           const bool last = atomicAdd(a.counters + c_lo, 1u) == (unsigned)(c_hi - c_lo);
           if (last) a.counters[c_lo] = 0;
           __threadfence();
@@ -448,14 +466,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         few_bar();
         finish = *s_last;
         if (finish) {
-          const float* p = a.part + (size_t)(2 * c_lo + 1) * kFewPart + row;
+          // four tokens and four CTAs at a time, so that the loads overlap (rows past T are loaded,
+          // never used)
 #pragma unroll
-          for (int t = 0; t < kFewRows; ++t) acc[t] = t < a.T ? __ldcg(p + t * 256) : 0.0f;
-          for (int i = c_lo + 1; i <= c_hi; ++i) {
-            p = a.part + (size_t)(2 * i) * kFewPart + row;
+          for (int t4 = 0; t4 < kFewRows; t4 += 4) {
+            if (t4 >= a.T) break;
+            const float* p = a.part + (size_t)(2 * c_lo + 1) * kFewPart + t4 * 256 + row;
+            float v[4];
 #pragma unroll
-            for (int t = 0; t < kFewRows; ++t)
-              if (t < a.T) acc[t] += __ldcg(p + t * 256);
+            for (int t = 0; t < 4; ++t) v[t] = __ldcg(p + t * 256);
+            p = a.part + (size_t)(2 * c_lo + 2) * kFewPart + t4 * 256 + row;
+            int i = c_lo + 1;
+            for (; i + 3 <= c_hi; i += 4, p += 8 * kFewPart) {
+              float n[4][4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) n[j][t] = __ldcg(p + j * 2 * kFewPart + t * 256);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) v[t] += n[j][t];
+            }
+            for (; i <= c_hi; ++i, p += 2 * kFewPart)
+#pragma unroll
+              for (int t = 0; t < 4; ++t) v[t] += __ldcg(p + t * 256);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t4 + t] = v[t];
           }
         }
       }
@@ -508,7 +545,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (*abort_flag) {
     // a wait gave up: let the copies still in flight land before the CTA's shared memory is released
     if (tid == 0) {
-      drain_ring(full_bar, a.stages, fills, 3, fills[3]);
+      drain_ring(full_bar, a.stages, fills, 3, min(fills[3], fills[4]));
       drain_ring(sf_full, a.stages, fills, MODE == FEW_DOWN ? 2 : 1, fills[2]);
     }
     __syncthreads();
