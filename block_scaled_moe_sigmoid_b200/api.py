@@ -118,28 +118,23 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _checked(name, t, dtype, shape, device):
-    """t's data pointer, after checks that a pointer alone cannot carry: type, shape, contiguity, device."""
+def _checked(name, t, dtype, shape, index):
+    """t's data pointer, after checks that a pointer alone cannot carry: type, shape, contiguity, device index."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {index}, got "
                          f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-class _OnDevice:
-    """The device of a call's tensors made current, and its stream the one that new outputs
-    belong to (a no-op where both already are)."""
+class _On:
+    """A device made current, and a stream: outputs allocated inside belong to it."""
 
-    def __init__(self, device, stream):
-        self.guards = []
-        if device.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {device}")
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
+    def __init__(self, index, stream):
+        if index < 0:
+            raise ValueError("expected CUDA tensors")
+        self.guards = [torch.cuda.device(index)] + ([torch.cuda.stream(stream)] if stream is not None else [])
 
     def __enter__(self):
         for g in self.guards:
@@ -148,6 +143,16 @@ class _OnDevice:
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
+
+
+def _elsewhere(index, stream):
+    """Whether a call on device `index` and `stream` needs _On around it."""
+    return stream is not None or index < 0 or index != torch.cuda.current_device()
+
+
+def _raw_stream(index):
+    """The handle of the current stream of a device."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _stream(stream=None):
@@ -313,30 +318,35 @@ def moe_add_rmsnorm_mxfp8(x, gamma, eps=1e-5, residual=None, residual_out=None, 
     Returns (r in the residual's type or None, xn bf16, q uint8 [rows, cols], scale uint8
     [rows, cols / 32]).  Outputs are allocated where not given; residual_out may be the residual
     itself.  with_xn / with_mx = False leave xn / (q, scale) out (None)."""
-    if x.dim() != 2:
-        raise ValueError(f"x: expected [rows, cols], got {tuple(x.shape)}")
-    rows, cols = x.shape
-    dev = x.device
-    rtype = MOE_TYPE_BF16 if residual is None else _type("residual", residual.dtype)
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out without a residual")
+    i = x.get_device()
+    if _elsewhere(i, stream):
+        with _On(i, stream):
+            return moe_add_rmsnorm_mxfp8(x, gamma, eps, residual, residual_out, xn, q, scale, with_xn, with_mx)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: expected [rows, cols], got {tuple(shape)}")
     if (xn is not None and not with_xn) or ((q is not None or scale is not None) and not with_mx):
         raise ValueError("an output was given that with_xn / with_mx leave out")
-    with _OnDevice(dev, stream):
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
-        if with_xn and xn is None:
-            xn = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-        if with_mx:
-            q = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if q is None else q
-            scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev) if scale is None else scale
-        _call("moe_add_rmsnorm_mxfp8", _checked("x", x, torch.bfloat16, (rows, cols), dev),
-              _checked("residual", residual, residual.dtype if residual is not None else None, (rows, cols), dev), rtype,
-              _checked("gamma", gamma, torch.float32, (cols,), dev), eps, rows, cols,
-              _checked("residual_out", residual_out, residual.dtype if residual is not None else None, (rows, cols), dev),
-              _checked("xn", xn, torch.bfloat16, (rows, cols), dev),
-              _checked("q", q, torch.uint8, (rows, cols), dev),
-              _checked("scale", scale, torch.uint8, (rows, cols // 32), dev), _stream(stream))
+    rows, cols = shape
+    blocks = (rows, cols // 32)
+    px = _checked("x", x, torch.bfloat16, shape, i)
+    rtype, pr, pro, pn, pq, ps = MOE_TYPE_BF16, None, None, None, None, None
+    if residual is not None:
+        rtype, pr = _type("residual", residual.dtype), _checked("residual", residual, residual.dtype, shape, i)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        pro = _checked("residual_out", residual_out, residual.dtype, shape, i)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if with_xn:
+        xn = torch.empty_like(x) if xn is None else xn
+        pn = _checked("xn", xn, torch.bfloat16, shape, i)
+    if with_mx:
+        q = torch.empty_like(x, dtype=torch.uint8) if q is None else q
+        scale = torch.empty_strided(blocks, (blocks[1], 1), dtype=torch.uint8, device=x.device) if scale is None else scale
+        pq, ps = _checked("q", q, torch.uint8, shape, i), _checked("scale", scale, torch.uint8, blocks, i)
+    _call("moe_add_rmsnorm_mxfp8", px, pr, rtype, _checked("gamma", gamma, torch.float32, (cols,), i), eps, rows, cols, pro,
+          pn, pq, ps, _raw_stream(i))
     return residual_out, xn, q, scale
 
 
@@ -373,42 +383,48 @@ def moe_linear_bytes(N, K):
 
 
 def moe_pack_linear_mxfp4(N, K, w, weights, stream=None):
-    with _OnDevice(w.device, None):
-        _call("moe_pack_linear_mxfp4", N, K, _checked("w", w, torch.float32, (N, K), weights.w.device),
-              ctypes.byref(weights.struct()), _stream(stream))
+    i = weights.w.get_device()
+    if _elsewhere(i, stream):
+        with _On(i, stream):
+            return moe_pack_linear_mxfp4(N, K, w, weights)
+    _call("moe_pack_linear_mxfp4", N, K, _checked("w", w, torch.float32, (N, K), i), ctypes.byref(weights.struct()),
+          _raw_stream(i))
 
 
 def moe_linear_mxfp4(linear, q, scale, weights, y=None, dtype=torch.bfloat16, stream=None):
     """y [T, N] (bf16 or fp32) = W x for MXFP8 rows q uint8 [T, K], scale uint8 [T, K / 32] and a
     LinearMXFP4 on `linear`, a handle of moe_linear_create for its shape."""
-    N, K, dev = weights.N, weights.K, weights.w.device
-    T = q.shape[0]
-    with _OnDevice(dev, stream):
-        if y is None:
-            y = torch.empty((T, N), dtype=dtype, device=dev)
-        _call("moe_linear_mxfp4", linear, _checked("q", q, torch.uint8, (T, K), dev),
-              _checked("scale", scale, torch.uint8, (T, K // 32), dev), T, ctypes.byref(weights.struct()),
-              _checked("y", y, y.dtype, (T, N), dev), _type("y", y.dtype), _stream(stream))
+    i = weights.w.get_device()
+    if _elsewhere(i, stream):
+        with _On(i, stream):
+            return moe_linear_mxfp4(linear, q, scale, weights, y, dtype)
+    N, K, T = weights.N, weights.K, q.shape[0]
+    if y is None:
+        y = torch.empty_strided((T, N), (N, 1), dtype=dtype, device=q.device)
+    _call("moe_linear_mxfp4", linear, _checked("q", q, torch.uint8, (T, K), i),
+          _checked("scale", scale, torch.uint8, (T, K // 32), i), T, ctypes.byref(weights.struct()),
+          _checked("y", y, y.dtype, (T, N), i), _type("y", y.dtype), _raw_stream(i))
     return y
 
 
 def moe_forward_decode(plan, x, idx, w, experts, shared=None, q=None, scale=None, y=None, stream=None):
     """The layer for up to 16 tokens x bf16 [T, d]; (q, scale) is their MXFP8 form where it is at
     hand, and x may then be None without a shared expert."""
-    T, d = (q if x is None else x).shape
-    dev = idx.device
-    k = idx.shape[1] if idx.dim() == 2 else -1
-    ex = experts.struct()
-    sh = shared.struct() if shared is not None else None
-    with _OnDevice(dev, stream):
-        if y is None:
-            y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-        _call("moe_forward_decode", plan, _checked("x", x, torch.bfloat16, (T, experts.d), dev),
-              _checked("q", q, torch.uint8, (T, experts.d), dev),
-              _checked("scale", scale, torch.uint8, (T, experts.d // 32), dev), T,
-              _checked("idx", idx, torch.int32, (T, k), dev), _checked("w", w, torch.float32, (T, k), dev),
-              ctypes.byref(ex), ctypes.byref(sh) if sh is not None else None,
-              _checked("y", y, torch.bfloat16, (T, d), dev), _stream(stream))
+    i = experts.w_gu.get_device()
+    if _elsewhere(i, stream):
+        with _On(i, stream):
+            return moe_forward_decode(plan, x, idx, w, experts, shared, q, scale, y)
+    routes = idx.shape
+    if len(routes) != 2:
+        raise ValueError(f"idx: expected [T, k], got {tuple(routes)}")
+    T, d = routes[0], experts.d
+    if y is None:
+        y = torch.empty_strided((T, d), (d, 1), dtype=torch.bfloat16, device=idx.device)
+    _call("moe_forward_decode", plan, _checked("x", x, torch.bfloat16, (T, d), i), _checked("q", q, torch.uint8, (T, d), i),
+          _checked("scale", scale, torch.uint8, (T, d // 32), i), T, _checked("idx", idx, torch.int32, routes, i),
+          _checked("w", w, torch.float32, routes, i), ctypes.byref(experts.struct()),
+          ctypes.byref(shared.struct()) if shared is not None else None, _checked("y", y, torch.bfloat16, (T, d), i),
+          _raw_stream(i))
     return y
 
 

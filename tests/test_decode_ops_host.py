@@ -131,13 +131,13 @@ def test_binding_refuses_what_a_pointer_cannot_carry():
         api.moe_add_rmsnorm_mxfp8(x, g, residual_out=x)
     with pytest.raises(ValueError):
         api.moe_add_rmsnorm_mxfp8(x, g, xn=x, with_xn=False)
-    dev = torch.device("cpu")
+    host = -1
     ok = torch.zeros(4, 8)
-    assert api._checked("t", None, torch.float32, (4, 8), dev) is None
-    assert api._checked("t", ok, torch.float32, (4, 8), dev) == ok.data_ptr()
+    assert api._checked("t", None, torch.float32, (4, 8), host) is None
+    assert api._checked("t", ok, torch.float32, (4, 8), host) == ok.data_ptr()
     for t, dtype, shape in ((ok.double(), torch.float32, (4, 8)), (ok, torch.float32, (8, 4)), (ok[:, ::2], torch.float32, (4, 4)),
                             (ok.t(), torch.float32, (8, 4))):
         with pytest.raises(ValueError):
-            api._checked("t", t, dtype, shape, dev)
+            api._checked("t", t, dtype, shape, host)
     with pytest.raises(ValueError):
-        api._checked("t", ok, torch.float32, (4, 8), torch.device("cuda", 0))
+        api._checked("t", ok, torch.float32, (4, 8), 0)
