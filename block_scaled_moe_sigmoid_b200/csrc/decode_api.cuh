@@ -31,6 +31,37 @@ cudaError_t launch_linear_gemm(int bn, const GemmArgs& a, const CUtensorMap& tA,
   return launch_gemm_cfg<KIND_MX, EPI, kBN, kStages>(a, tA, tB, grid, s);
 }
 
+// The norm's variants.  A thread holds V vectors of 8 elements: one where a row fits 1024 threads so,
+// else 2 or 4.  The streaming kernel pays where a CTA per row is so wide that only two fit an SM, and
+// there are rows enough for more than one turn: 8192 x 7168 85 us against 106, 400 x 7168 7.9 against
+// 8.6; but 8192 x 4096 59 against 51 (a CTA of 512 threads has three others beside it).
+constexpr int kNormStreamVecs = 512;
+template <int RES, int V>
+cudaError_t launch_norm_rows(const NormArgs& a, cudaStream_t s) {
+  const int nvec = a.cols / 8, team = ((nvec + V - 1) / V + 31) / 32 * 32, per_cta = std::max(1, 128 / team);
+  return launch_k(add_rmsnorm_mxfp8_kernel<RES, V>, (unsigned)((a.rows + per_cta - 1) / per_cta), dim3(team, per_cta), 0, s, a);
+}
+template <int RES>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
+  const int nvec = a.cols / 8;
+  if constexpr (RES != NORM_RES_F32) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return cudaErrorInvalidDevice;
+    const int team = ((nvec + 1) / 2 + 31) / 32 * 32, grid = sms * (team > 512 ? 1 : 2);
+    if (nvec > kNormStreamVecs && nvec <= 2048 && a.rows > grid) {
+      auto kern = add_rmsnorm_mxfp8_stream_kernel<RES, 2>;
+      static std::atomic<uint64_t> done{0};
+      const cudaError_t e = ensure_smem_attr(kern, kNormDepth * 2 * 32 * 1024, done);
+      if (e != cudaSuccess) return e;
+      return launch_k(kern, grid, team, kNormDepth * 2 * (RES == NORM_RES_BF16 ? 32 : 16) * team, s, a);
+    }
+  }
+  if (nvec > 2048) return launch_norm_rows<RES, 4>(a, s);
+  if (nvec > 1024) return launch_norm_rows<RES, 2>(a, s);
+  return launch_norm_rows<RES, 1>(a, s);
+}
+
 }  // namespace
 
 struct moe_linear_s {
@@ -60,25 +91,12 @@ moe_status_t moe_add_rmsnorm_mxfp8(const void* x, const void* residual, moe_type
       !aligned(q, 16))
     return MOE_ERR_ALIGNMENT;
   NormArgs a{(const uint16_t*)x, residual, gamma, eps, rows, cols, residual_out, (uint16_t*)xn, q, scale};
-  const int nvec = cols / 8;
-  const int V = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4;
-  const int team = ((nvec + V - 1) / V + 31) / 32 * 32;
-  const int per_cta = std::max(1, 128 / team);
-  const dim3 block(team, per_cta);
-  const unsigned grid = (unsigned)((rows + per_cta - 1) / per_cta);
-  cudaError_t e = cudaSuccess;
-  auto go = [&](auto kern) { e = launch_k(kern, grid, block, 0, S(stream), a); };
   const int res = !residual ? NORM_RES_NONE : residual_type == MOE_TYPE_BF16 ? NORM_RES_BF16 : NORM_RES_F32;
-  switch (res * 8 + V) {
-    case NORM_RES_NONE * 8 + 1: go(add_rmsnorm_mxfp8_kernel<NORM_RES_NONE, 1>); break;
-    case NORM_RES_NONE * 8 + 2: go(add_rmsnorm_mxfp8_kernel<NORM_RES_NONE, 2>); break;
-    case NORM_RES_NONE * 8 + 4: go(add_rmsnorm_mxfp8_kernel<NORM_RES_NONE, 4>); break;
-    case NORM_RES_BF16 * 8 + 1: go(add_rmsnorm_mxfp8_kernel<NORM_RES_BF16, 1>); break;
-    case NORM_RES_BF16 * 8 + 2: go(add_rmsnorm_mxfp8_kernel<NORM_RES_BF16, 2>); break;
-    case NORM_RES_BF16 * 8 + 4: go(add_rmsnorm_mxfp8_kernel<NORM_RES_BF16, 4>); break;
-    case NORM_RES_F32 * 8 + 1: go(add_rmsnorm_mxfp8_kernel<NORM_RES_F32, 1>); break;
-    case NORM_RES_F32 * 8 + 2: go(add_rmsnorm_mxfp8_kernel<NORM_RES_F32, 2>); break;
-    default: go(add_rmsnorm_mxfp8_kernel<NORM_RES_F32, 4>); break;
+  cudaError_t e;
+  switch (res) {
+    case NORM_RES_NONE: e = launch_norm<NORM_RES_NONE>(a, S(stream)); break;
+    case NORM_RES_BF16: e = launch_norm<NORM_RES_BF16>(a, S(stream)); break;
+    default: e = launch_norm<NORM_RES_F32>(a, S(stream)); break;
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

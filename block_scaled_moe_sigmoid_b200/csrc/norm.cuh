@@ -50,8 +50,67 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// blockDim = (threads per row, a multiple of 32; rows per CTA).  Thread i of a row's team holds
-// the 8-element vectors i, i + team, ... (V of them): 4 neighbouring lanes hold a 32-element block.
+// r of one vector from its x and residual; a bf16 r is stored here where it is wanted.
+template <int RES>
+__device__ __forceinline__ void norm_add(const NormArgs& a, size_t base, int c, const uint4& x, const uint4& r0, const uint4& r1,
+                                         float (&v)[8]) {
+  unpack_bf16x8(x, v);
+  if constexpr (RES == NORM_RES_BF16) {
+    float r[8];
+    unpack_bf16x8(r0, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += r[j];
+    const uint4 p = pack_bf16x8(v);
+    unpack_bf16x8(p, v);
+    if (a.res_out) ((uint4*)((uint16_t*)a.res_out + base))[c] = p;
+  } else if constexpr (RES == NORM_RES_F32) {
+    const uint32_t r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(r[j]);
+  }
+}
+
+// A warp's part of the row's sum of squares.
+__device__ __forceinline__ float norm_warp_sum(float ss) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  return ss;
+}
+
+// xn and the MX codes of one vector (4 neighbouring lanes hold a 32-element block).
+__device__ __forceinline__ void norm_store(const NormArgs& a, size_t base, int c, bool ok, float inv, float (&v)[8]) {
+  if (ok) {
+    const float4* g = (const float4*)a.gamma + 2 * c;
+    const float4 lo = __ldg(g), hi = __ldg(g + 1);
+    v[0] *= inv * lo.x; v[1] *= inv * lo.y; v[2] *= inv * lo.z; v[3] *= inv * lo.w;
+    v[4] *= inv * hi.x; v[5] *= inv * hi.y; v[6] *= inv * hi.z; v[7] *= inv * hi.w;
+  }
+  const uint4 p = pack_bf16x8(v);
+  if (ok && a.xn) ((uint4*)(a.xn + base))[c] = p;
+  if (a.q) {
+    unpack_bf16x8(p, v);
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int e = mx_scale_exp(amax, 8);
+    const float s = pow2_neg(e);
+    uint32_t w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      w[j] = cvt_e4m3x2(v[4 * j] * s, v[4 * j + 1] * s) | (cvt_e4m3x2(v[4 * j + 2] * s, v[4 * j + 3] * s) << 16);
+    if (ok) {
+      ((uint2*)(a.q + base))[c] = make_uint2(w[0], w[1]);
+      if ((c & 3) == 0) a.scale[(base >> 5) + (c >> 2)] = (uint8_t)(e + 127);
+    }
+  }
+}
+
+// Thread i of a row's team (a multiple of 32 threads) holds the 8-element vectors i, i + team, ... (V of
+// them).  The row's sum of squares is taken per thread, per warp, per team: a fixed order.
+
+// A row per team, straight through registers; blockDim = (team, rows per CTA).
 template <int RES, int V>
 __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormArgs a) {
   __shared__ float part[32];
@@ -69,38 +128,28 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormArgs 
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
     if (c < nvec) {
-      unpack_bf16x8(((const uint4*)(a.x + base))[c], v[i]);
-      if constexpr (RES == NORM_RES_BF16) {
-        float r[8];
-        unpack_bf16x8(((const uint4*)((const uint16_t*)a.res + base))[c], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
-        const uint4 p = pack_bf16x8(v[i]);
-        unpack_bf16x8(p, v[i]);
-        if (a.res_out) ((uint4*)((uint16_t*)a.res_out + base))[c] = p;
-      } else if constexpr (RES == NORM_RES_F32) {
-        const float4* src = (const float4*)((const float*)a.res + base) + 2 * c;
-        const float4 lo = src[0], hi = src[1];
-        v[i][0] += lo.x; v[i][1] += lo.y; v[i][2] += lo.z; v[i][3] += lo.w;
-        v[i][4] += hi.x; v[i][5] += hi.y; v[i][6] += hi.z; v[i][7] += hi.w;
-        if (a.res_out) {
-          float4* dst = (float4*)((float*)a.res_out + base) + 2 * c;
-          dst[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-          dst[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
-        }
+      uint4 r0 = {}, r1 = {};
+      if constexpr (RES == NORM_RES_BF16) r0 = ((const uint4*)((const uint16_t*)a.res + base))[c];
+      if constexpr (RES == NORM_RES_F32) {
+        const uint4* src = (const uint4*)((const float*)a.res + base) + 2 * c;
+        r0 = src[0];
+        r1 = src[1];
+      }
+      norm_add<RES>(a, base, c, ((const uint4*)(a.x + base))[c], r0, r1, v[i]);
+      if (RES == NORM_RES_F32 && a.res_out) {
+        float4* dst = (float4*)((float*)a.res_out + base) + 2 * c;
+        dst[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        dst[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
       }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
   }
   if (!a.xn && !a.q) return;   // the same for the whole grid
-  // the row's sum of squares, in a fixed order: per thread, per warp, per team
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  ss = norm_warp_sum(ss);
   const int wpr = team >> 5;   // warps per row
   if (wpr > 1) {
-    const int w = threadIdx.y * wpr + (threadIdx.x >> 5);
-    if ((threadIdx.x & 31) == 0) part[w] = ss;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.y * wpr + (threadIdx.x >> 5)] = ss;
     __syncthreads();
     ss = 0.0f;
     for (int i = 0; i < wpr; ++i) ss += part[threadIdx.y * wpr + i];
@@ -109,33 +158,76 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormArgs 
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = threadIdx.x + i * team;
-    const bool ok = c < nvec;
-    if (ok) {
-      const float4* g = (const float4*)a.gamma + 2 * c;
-      const float4 lo = __ldg(g), hi = __ldg(g + 1);
-      v[i][0] *= inv * lo.x; v[i][1] *= inv * lo.y; v[i][2] *= inv * lo.z; v[i][3] *= inv * lo.w;
-      v[i][4] *= inv * hi.x; v[i][5] *= inv * hi.y; v[i][6] *= inv * hi.z; v[i][7] *= inv * hi.w;
-    }
-    const uint4 p = pack_bf16x8(v[i]);
-    if (ok && a.xn) ((uint4*)(a.xn + base))[c] = p;
-    if (a.q) {
-      unpack_bf16x8(p, v[i]);
-      float amax = 0.0f;
+    norm_store(a, base, c, c < nvec, inv, v[i]);
+  }
+}
+
+// Many wide rows: a resident grid walks the rows, a CTA each, and every thread keeps the loads of its
+// next three rows in flight (cp.async into shared memory that only it reads, so nothing waits but the row's sum).
+// 8192 x 7168 with a bf16 residual: 85 us, 6.2 TB/s, where a CTA per row takes 106 us (its loads stop
+// while it reduces and stores).  With an fp32 residual a CTA per row has enough loads in flight (125 us,
+// 6.1 TB/s) and the ring would hold too few rows (134 us).
+constexpr int kNormDepth = 3;
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+template <int RES, int V>
+__global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_stream_kernel(const NormArgs a) {
+  static_assert(RES != NORM_RES_F32, "fp32 residuals take a CTA per row");
+  constexpr int PIECES = RES == NORM_RES_BF16 ? 2 : 1;   // 16-byte pieces of a vector: x, residual
+  extern __shared__ uint4 ring[];                        // [kNormDepth][V][PIECES][threads]
+  __shared__ float part[2][32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int team = blockDim.x, tid = threadIdx.x, nvec = a.cols >> 3;
+  auto slot = [&](int st, int i, int pc) { return ring + ((st * V + i) * PIECES + pc) * team + tid; };
+  auto load = [&](long long row, int st) {
+    if (row < a.rows) {
+      const size_t base = (size_t)row * a.cols;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int e = mx_scale_exp(amax, 8);
-      const float s = pow2_neg(e);
-      uint32_t w[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        w[j] = cvt_e4m3x2(v[i][4 * j] * s, v[i][4 * j + 1] * s) |
-               (cvt_e4m3x2(v[i][4 * j + 2] * s, v[i][4 * j + 3] * s) << 16);
-      if (ok) {
-        ((uint2*)(a.q + base))[c] = make_uint2(w[0], w[1]);
-        if ((c & 3) == 0) a.scale[(base >> 5) + (c >> 2)] = (uint8_t)(e + 127);
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * team;
+        if (c >= nvec) continue;
+        cp_async_16(slot(st, i, 0), (const uint4*)(a.x + base) + c);
+        if constexpr (RES == NORM_RES_BF16) cp_async_16(slot(st, i, 1), (const uint4*)((const uint16_t*)a.res + base) + c);
       }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int d = 0; d < kNormDepth; ++d) load(blockIdx.x + (long long)d * gridDim.x, d);
+  int st = 0, turn = 0;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const size_t base = (size_t)row * a.cols;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kNormDepth - 1) : "memory");
+    float v[V][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * team;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+      if (c < nvec) {
+        uint4 r0 = {};
+        if constexpr (RES == NORM_RES_BF16) r0 = *slot(st, i, 1);
+        norm_add<RES>(a, base, c, *slot(st, i, 0), r0, r0, v[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    load(row + (long long)kNormDepth * gridDim.x, st);
+    if (++st == kNormDepth) st = 0;
+    if (!a.xn && !a.q) continue;   // the same for the whole grid
+    ss = norm_warp_sum(ss);
+    if ((tid & 31) == 0) part[turn][tid >> 5] = ss;
+    __syncthreads();   // the next turn writes the other half: one barrier a row is enough
+    ss = 0.0f;
+    for (int i = 0; i < team >> 5; ++i) ss += part[turn][i];
+    const float inv = rsqrtf(ss / (float)a.cols + a.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * team;
+      norm_store(a, base, c, c < nvec, inv, v[i]);
     }
   }
 }
