@@ -13,7 +13,8 @@ bool make_few_maps(CUtensorMap* mW, CUtensorMap* mX, const void* w, uint64_t til
 
 // Launch few_kernel with as many pipeline stages as fit.
 template <int MODE, int ACT>
-cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, const CUtensorMap& tX, int grid, cudaStream_t s) {
+cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, const CUtensorMap& tX, const CUtensorMap& tSW, const CUtensorMap& tSX,
+                       int grid, cudaStream_t s) {
   auto kern = few_kernel<MODE, ACT>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_attr(kern, kFewSmemMax, done);
@@ -21,7 +22,7 @@ cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, const CUtensorMap& tX, 
   const int fixed = few_smem(MODE, a.T, a.k, a.k_tiles, 0).total;
   a.stages = std::min(kFewMaxStages, (kFewSmemMax - fixed) / (kFewStage + kFewSF));
   if (a.stages < 3) return cudaErrorInvalidValue;
-  return launch_k(kern, grid, kFewThreads, few_smem(MODE, a.T, a.k, a.k_tiles, a.stages).total, s, a, tW, tX);
+  return launch_k(kern, grid, kFewThreads, few_smem(MODE, a.T, a.k, a.k_tiles, a.stages).total, s, a, tW, tX, tSW, tSX);
 }
 
 // The dense block-scaled GEMM in its two token-tile configurations.
@@ -219,7 +220,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
     a.counters = p->at<unsigned int>(p->o_cnt);
     a.status = p->at<unsigned int>(p->o_status);
     const int grid = std::min(m_tiles * k_tiles, std::min(p->num_sms, kFewMaxCtas));
-    return launch_few<FEW_LINEAR, 0>(a, tW, tX, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_few<FEW_LINEAR, 0>(a, tW, tX, tW, tX, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   // more rows: the block-scaled GEMM on one dense group
   const int bn = moe_linear_s::tile_rows(T), nt = (T + bn - 1) / bn;
@@ -292,9 +293,6 @@ moe_status_t moe_forward_decode(moe_plan_t p, const void* x, const uint8_t* q, c
   if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
   cudaStream_t s = S(stream);
   const int d = p->d, E = p->E, I = p->I;
-  float* ys = nullptr;
-  const moe_status_t st = run_shared(p, x, T, sh, kBNSmall, s, &ys);
-  if (st != MOE_OK) return st;
   FewArgs a;
   memset(&a, 0, sizeof(a));
   a.T = T;
@@ -318,28 +316,45 @@ moe_status_t moe_forward_decode(moe_plan_t p, const void* x, const uint8_t* q, c
     q = xq;
     scale = xs;
   }
-  CUtensorMap tW, tX;
-  // gate/up, GLU, MXFP8 rows of the hidden values
+  CUtensorMap tW, tX, tSW, tSX;
+  const int Is = p->Is;
+  p->last_shared_split = p->last_shared_split_dn = 0;
+  // gate/up, GLU, MXFP8 rows of the hidden values; the shared expert's hidden values
   a.m_tiles = I / 128;
   a.k_tiles = d / 128;
   a.sf = (const uint8_t*)ex->s_gu;
   a.xs = scale;
   if (!make_few_maps(&tW, &tX, ex->w_gu, (uint64_t)E * a.m_tiles * a.k_tiles, q, T, d)) return MOE_ERR_CUDA;
+  tSW = tW;
+  tSX = tX;
+  if (sh) {
+    a.sh_tiles = Is / 128;
+    a.sh_steps = d / 64;
+    a.hsh = p->at<__nv_bfloat16>(p->o_hsh);
+    if (!make_map(&tSW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sh->w_gu, d, 2ull * Is, (uint64_t)d * 2, 64, 256) ||
+        !make_map(&tSX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, d, T, (uint64_t)d * 2, 64, kFewRows))
+      return MOE_ERR_CUDA;
+  }
   p->prof.begin(MOE_STAGE_GATE_UP, s);
-  if ((p->act == MOE_ACT_CLAMPED_SWIGLU ? launch_few<FEW_GLU, 1>(a, tW, tX, grid, s)
-                                        : launch_few<FEW_GLU, 0>(a, tW, tX, grid, s)) != cudaSuccess)
+  if ((p->act == MOE_ACT_CLAMPED_SWIGLU ? launch_few<FEW_GLU, 1>(a, tW, tX, tSW, tSX, grid, s)
+                                        : launch_few<FEW_GLU, 0>(a, tW, tX, tSW, tSX, grid, s)) != cudaSuccess)
     return MOE_ERR_CUDA;
   p->prof.end(s);
-  // down, weighted combine, shared output
+  // down products, weighted combine, the shared expert's down product
   a.m_tiles = (d + 255) / 256;
   a.k_tiles = I / 128;
   a.rows = d;
   a.sf = (const uint8_t*)ex->s_dn;
-  a.ys = ys;
   a.y = y;
   if (!make_few_maps(&tW, &tX, ex->w_dn, (uint64_t)E * a.m_tiles * a.k_tiles, a.hq, (uint64_t)T * a.k * T, I)) return MOE_ERR_CUDA;
+  if (sh) {
+    a.sh_steps = Is / 64;
+    if (!make_map(&tSW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sh->w_dn, Is, d, (uint64_t)Is * 2, 64, 256) ||
+        !make_map(&tSX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.hsh, Is, T, (uint64_t)Is * 2, 64, kFewRows))
+      return MOE_ERR_CUDA;
+  }
   p->prof.begin(MOE_STAGE_DOWN, s);
-  if (launch_few<FEW_DOWN, 0>(a, tW, tX, grid, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_few<FEW_DOWN, 0>(a, tW, tX, tSW, tSX, grid, s) != cudaSuccess) return MOE_ERR_CUDA;
   p->prof.end(s);
   p->last_T = T;
   return MOE_OK;

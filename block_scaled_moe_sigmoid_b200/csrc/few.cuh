@@ -2,7 +2,8 @@
 //
 //   FEW_LINEAR  y[t] = W x[t]                                    one matrix, x in MXFP8
 //   FEW_GLU     h[t,e] = MX(glu(Wg x[t], Wu x[t]))               the experts e = idx[t][j]
-//   FEW_DOWN    y[t] = bf16(ys[t] + sum_j w[t][j] Wd h[t,j])     the same experts
+//               hs[t] = bf16(glu(Vg x[t], Vu x[t]))              the shared expert, bf16
+//   FEW_DOWN    y[t] = bf16(Vd hs[t] + sum_j w[t][j] Wd h[t,j])  the same experts
 //
 // With so few rows every weight byte is used once and the bytes are the cost: 17/32 byte per
 // weight at the copy rate of the memory.  The work is one list of steps, a step being one 256-row
@@ -18,6 +19,11 @@
 // other, each through an accumulator of its own that the epilogue adds, times the token's weight, to
 // fp32 registers.
 //
+// The shared expert's bf16 weights are steps of the same lists: 256 rows x 64 columns, 32 KB, counted
+// as two (a boundary between two CTAs that falls inside one gives it to the first).  In FEW_GLU they
+// are tiles of their own after the routed ones, in FEW_DOWN they end each tile's contraction.  Their
+// MMAs are kind::f16; everything else is common.
+//
 // A step's products are eight tcgen05.mma kind::mxf8f6f4.block_scale (two 128-row halves x four
 // 32-column blocks, N = 16 tokens), which decode the codes and apply the scales themselves.  The same
 // products on mma.sync were measured too: making f16 operands out of the codes then takes more than
@@ -28,6 +34,8 @@
 // 128-row half each (one thread forms and issues an instruction in about 90 cycles, and eight of them
 // would take longer than the step's load), warps 2 to 9 run the epilogue, a thread per weight row.
 #pragma once
+#include <type_traits>
+
 #include "gemm.cuh"
 #include "kernels.cuh"
 
@@ -58,9 +66,10 @@ struct FewArgs {
   const int* idx;
   const float* w;
   const uint8_t* xs;      // FEW_LINEAR, FEW_GLU: token scales [T][4 k_tiles]
+  int sh_tiles, sh_steps; // shared expert: m-tiles (FEW_GLU), 64-column steps of a tile's contraction (0: none)
+  __nv_bfloat16* hsh;     // FEW_GLU: its hidden values [T][128 sh_tiles]
   uint8_t* hq;            // codes of h, [used expert][T][128 k-tiles of the down product]
   uint8_t* hs;            // scale atoms of h, [used expert][k-tile][512]
-  const float* ys;        // shared expert's output, or NULL
   void* y;
   int y_f32;
   float* part;            // [2 per CTA][T][256]
@@ -107,7 +116,8 @@ __device__ __forceinline__ void few_bar() {   // the epilogue warps
 template <int MODE, int ACT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ CUtensorMap tmW,
-               const __grid_constant__ CUtensorMap tmX) {
+               const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSW,
+               const __grid_constant__ CUtensorMap tmSX) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const FewSmem L = few_smem(MODE, a.T, a.k, a.k_tiles, a.stages);
@@ -151,6 +161,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     fence_mbar_init();
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmX);
+    if (MODE != FEW_LINEAR && a.sh_steps) {
+      prefetch_tmap(&tmSW);
+      prefetch_tmap(&tmSX);
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), kFewTmemCols);
@@ -213,26 +227,53 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __syncthreads();
   }
 
-  // this CTA's steps [s0, s1) of tiles x KT
-  const int tiles = MODE == FEW_GLU ? used * a.m_tiles : a.m_tiles;
-  const int KT = MODE == FEW_DOWN ? used * a.k_tiles : a.k_tiles;
-  const int total = tiles * KT;
-  const int unit = few_unit(tiles, KT, gridDim.x);      // a CTA's steps are whole units
+  // The list of steps, and this CTA's part [s0, s1) of it, in units of one routed step.
+  const int SS = MODE == FEW_LINEAR ? 0 : 2 * a.sh_steps;                    // of a tile's shared part
+  const int RT = MODE == FEW_DOWN ? used * a.k_tiles : a.k_tiles;            // of a tile's routed part
+  const int KT = MODE == FEW_DOWN ? RT + SS : RT;                            // of a tile (FEW_GLU: a routed one)
+  const int routed = MODE == FEW_GLU ? used * a.m_tiles * RT : a.m_tiles * KT;
+  const int total = routed + (MODE == FEW_GLU ? a.sh_tiles * SS : 0);
+  const int unit = SS ? 1 : few_unit(MODE == FEW_GLU ? used * a.m_tiles : a.m_tiles, KT, gridDim.x);   // that stay together
   const long long units = total / max(unit, 1);
-  const long long G = min(units, (long long)gridDim.x);
+  // at least four steps for a CTA where tiles are split
+  const long long G = min(unit == KT ? units : max(units / 4, min(units, 1ll)), (long long)gridDim.x);
   const int c = blockIdx.x;
   const int s0 = c < G ? (int)(c * units / G) * unit : 0, s1 = c < G ? (int)((c + 1) * units / G) * unit : 0;
-  // A run: consecutive steps of one matrix and one tile, accumulated in TMEM.  [kb, kb + n) are its K
-  // tiles, kk the first one's place in the tile's contraction.
-  struct Run { int tile, u, m, kk, kb, n; };
+  // A run: consecutive steps of one matrix and one tile, accumulated in TMEM: K tiles [kb, kb + n).
+  // The tile is [t0, t0 + len) in the list, and its last step begins at t0 + last.
+  struct Run { int tile, u, m, kb, n, next, t0, len, last; bool shared; };
   auto run_at = [&](int s) {
     Run r;
-    r.tile = s / KT;
-    r.kk = s - r.tile * KT;
-    r.u = MODE == FEW_GLU ? r.tile / a.m_tiles : MODE == FEW_DOWN ? r.kk / a.k_tiles : 0;
-    r.m = MODE == FEW_GLU ? r.tile - r.u * a.m_tiles : r.tile;
-    r.kb = MODE == FEW_DOWN ? r.kk - r.u * a.k_tiles : r.kk;
-    r.n = min(a.k_tiles - r.kb, s1 - s);
+    r.u = 0;
+    r.shared = false;
+    int kk;   // place in the tile
+    if (MODE == FEW_GLU && s >= routed) {
+      r.shared = true;
+      r.len = SS;
+      r.tile = (s - routed) / SS;
+      r.t0 = routed + r.tile * SS;
+      r.m = r.tile;
+      kk = s - r.t0;
+    } else {
+      r.len = KT;
+      r.tile = s / KT;
+      r.t0 = r.tile * KT;
+      r.m = r.tile;
+      kk = s - r.t0;
+      if (MODE == FEW_GLU) {
+        r.u = r.tile / a.m_tiles;
+        r.m = r.tile - r.u * a.m_tiles;
+      } else if (MODE == FEW_DOWN) {
+        r.shared = kk >= RT;
+        if (r.shared) kk -= RT;
+        else r.u = kk / a.k_tiles, kk -= r.u * a.k_tiles;
+      }
+    }
+    const int room = min(r.shared ? SS - kk : a.k_tiles - kk, s1 - s);
+    r.kb = r.shared ? (kk + 1) >> 1 : kk;
+    r.n = r.shared ? ((kk + room + 1) >> 1) - r.kb : room;   // 0: the second half of a step
+    r.next = s + room;
+    r.last = r.len - ((MODE == FEW_GLU ? r.shared : SS > 0) ? 2 : 1);
     return r;
   };
 
@@ -245,20 +286,30 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       bool ok = true;
       for (int s = s0; s < s1 && ok;) {
         const Run r = run_at(s);
-        const int e = MODE == FEW_LINEAR ? 0 : elist[r.u];
+        const int e = MODE == FEW_LINEAR || r.shared ? 0 : elist[r.u];
         const size_t blk = ((size_t)e * a.m_tiles + r.m) * a.k_tiles + r.kb;
-        for (int i = 0; i < r.n; ++i) {
-          ok = mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, a.status, abort_flag);
-          if (!ok) break;
-          const uint32_t sb = smem_u32(sf_full + stage), fb = smem_u32(full_bar + stage);
-          mbar_arrive_expect_tx(sb, 1024);
-          bulk_load(smem_u32(smem + L.sf + stage * kFewSF), a.sf + (blk + i) * 1024, 1024, sb);
-          mbar_arrive_expect_tx(fb, kFewTile);
-          tma_load_2d(smem_u32(smem + stage * kFewStage), &tmW, fb, 0, (int)((blk + i) * 256), pol);
-          ++nfill;
-          if (++stage == a.stages) { stage = 0; phase ^= 1; }
-        }
-        s += r.n;
+        auto run_steps = [&](auto shared) {
+          for (int i = 0; i < r.n; ++i) {
+            ok = mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, a.status, abort_flag);
+            if (!ok) return;
+            const uint32_t sb = smem_u32(sf_full + stage), fb = smem_u32(full_bar + stage), dst = smem_u32(smem + stage * kFewStage);
+            if constexpr (decltype(shared)::value) {
+              mbar_arrive(sb);
+              mbar_arrive_expect_tx(fb, kFewATile);
+              tma_load_2d(dst, &tmSW, fb, (r.kb + i) * 64, r.m * 256, pol);
+            } else {
+              mbar_arrive_expect_tx(sb, 1024);
+              bulk_load(smem_u32(smem + L.sf + stage * kFewSF), a.sf + (blk + i) * 1024, 1024, sb);
+              mbar_arrive_expect_tx(fb, kFewTile);
+              tma_load_2d(dst, &tmW, fb, 0, (int)((blk + i) * 256), pol);
+            }
+            ++nfill;
+            if (++stage == a.stages) { stage = 0; phase ^= 1; }
+          }
+        };
+        if (MODE != FEW_LINEAR && r.shared) run_steps(std::true_type{});
+        else run_steps(std::false_type{});
+        s = r.next;
       }
       fills[0] = nfill;
     }
@@ -277,6 +328,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           ok = mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, a.status, abort_flag);
           if (!ok) break;
           const uint32_t fb = smem_u32(full_bar + stage);
+          if (MODE != FEW_LINEAR && r.shared) {
+            if (MODE == FEW_DOWN) mbar_arrive(smem_u32(sf_full + stage));
+            mbar_arrive_expect_tx(fb, kFewBTile);
+            tma_load_2d(smem_u32(smem + stage * kFewStage + kFewATile), &tmSX, fb, (r.kb + i) * 64, 0, pol);
+            ++nfill;
+            if (++stage == a.stages) { stage = 0; phase ^= 1; }
+            continue;
+          }
           if constexpr (MODE == FEW_DOWN) {
             const uint32_t sb = smem_u32(sf_full + stage);
             mbar_arrive_expect_tx(sb, 512);
@@ -290,7 +349,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           ++nfill;
           if (++stage == a.stages) { stage = 0; phase ^= 1; }
         }
-        s += r.n;
+        s = r.next;
       }
       fills[1] = nfill;
     }
@@ -305,6 +364,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     bool ok = true;
     for (int s = s0; s < s1 && ok;) {
       const Run r = run_at(s);
+      if (MODE != FEW_LINEAR && r.shared) {   // no scales
+        for (int i = 0; i < r.n; ++i) {
+          int got = 1;
+          if (lane == 0) got = mbar_wait(smem_u32(sf_full + stage), phase, a.status, abort_flag);
+          ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(smem_u32(full_bar + stage));
+          ++nfill;
+          if (++stage == a.stages) { stage = 0; phase ^= 1; }
+        }
+        s = r.next;
+        continue;
+      }
       for (int i = 0; i < r.n; ++i) {
         int got = 1;
         if (lane == 0) got = mbar_wait(smem_u32(sf_full + stage), phase, a.status, abort_flag);
@@ -331,7 +403,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ++nfill;
         if (++stage == a.stages) { stage = 0; phase ^= 1; }
       }
-      s += r.n;
+      s = r.next;
     }
     if (lane == 0) {
       tc_commit(smem_u32(drain_sf));   // every copy lands before TMEM is released
@@ -352,44 +424,55 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       bool ok = true;
       for (int s = s0; s < s1 && ok;) {
         const Run r = run_at(s);
+        if (r.n == 0) { s = r.next; continue; }
         const int abuf = nrun & 1;
         const uint32_t acc_t = tmem_base + 32 * abuf + kFewRows * h;
-        auto issue_stage = [&](int st, uint32_t acc0) {
-          const uint64_t a_desc = desc0 + (uint64_t)((st * kFewStage + h * 16384) >> 4);
-          const uint64_t b_desc = desc0 + (uint64_t)((st * kFewStage + kFewATile) >> 4);
-          const uint32_t tsf = tmem_base + 64 + 16 * st;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_mxf8f6f4(acc_t, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4), idesc[j],
-                         (tsf + 4 * h) | ((uint32_t)j << 30), (tsf + 8) | ((uint32_t)j << 30), j > 0 ? 1u : acc0);
-        };
         // the accumulator is free once the epilogue has drained the run before the last one
         ok = mbar_wait(smem_u32(acc_empty + abuf), (uint32_t)(nrun >> 1 & 1) ^ 1u, a.status, abort_flag);
         if (!ok) break;
-        for (int i = 0; i < r.n;) {
-          const int stage2 = stage + 1 == a.stages ? 0 : stage + 1;
-          const uint32_t phase2 = stage + 1 == a.stages ? phase ^ 1u : phase;
-          ok = mbar_wait(smem_u32(full_bar + stage), phase, a.status, abort_flag);
-          if (!ok) break;
-          // a second stage in the same round where it has landed already
-          const bool two = i + 1 < r.n && mbar_try_wait(smem_u32(full_bar + stage2), phase2);
-          tc_fence_after();
-          issue_stage(stage, i > 0 ? 1u : 0u);
-          tc_commit(smem_u32(empty_bar + stage));
-          if (two) {
-            issue_stage(stage2, 1u);
-            tc_commit(smem_u32(empty_bar + stage2));
+        // the loop is compiled once for each kind: the issue rate hangs on what this one thread executes
+        auto run_steps = [&](auto shared) {
+          auto issue_stage = [&](int st, uint32_t acc0) {
+            const uint64_t a_desc = desc0 + (uint64_t)((st * kFewStage + h * 16384) >> 4);
+            const uint64_t b_desc = desc0 + (uint64_t)((st * kFewStage + kFewATile) >> 4);
+            const uint32_t tsf = tmem_base + 64 + 16 * st;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (decltype(shared)::value)
+                mma_bf16(acc_t, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4), idesc_bf16(128, kFewRows),
+                         j > 0 ? 1u : acc0);
+              else
+                mma_mxf8f6f4(acc_t, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4), idesc[j],
+                             (tsf + 4 * h) | ((uint32_t)j << 30), (tsf + 8) | ((uint32_t)j << 30), j > 0 ? 1u : acc0);
+            }
+          };
+          for (int i = 0; i < r.n;) {
+            const int stage2 = stage + 1 == a.stages ? 0 : stage + 1;
+            const uint32_t phase2 = stage + 1 == a.stages ? phase ^ 1u : phase;
+            ok = mbar_wait(smem_u32(full_bar + stage), phase, a.status, abort_flag);
+            if (!ok) return;
+            // a second stage in the same round where it has landed already
+            const bool two = i + 1 < r.n && mbar_try_wait(smem_u32(full_bar + stage2), phase2);
+            tc_fence_after();
+            issue_stage(stage, i > 0 ? 1u : 0u);
+            tc_commit(smem_u32(empty_bar + stage));
+            if (two) {
+              issue_stage(stage2, 1u);
+              tc_commit(smem_u32(empty_bar + stage2));
+            }
+            i += two ? 2 : 1;
+            nfill += two ? 2 : 1;
+            stage = stage2;
+            phase = phase2;
+            if (two && ++stage == a.stages) { stage = 0; phase ^= 1; }
           }
-          i += two ? 2 : 1;
-          nfill += two ? 2 : 1;
-          stage = stage2;
-          phase = phase2;
-          if (two && ++stage == a.stages) { stage = 0; phase ^= 1; }
-        }
+        };
+        if (MODE != FEW_LINEAR && r.shared) run_steps(std::true_type{});
+        else run_steps(std::false_type{});
         if (!ok) break;
         tc_commit(smem_u32(acc_full + abuf));
         ++nrun;
-        s += r.n;
+        s = r.next;
       }
       tc_commit(smem_u32(drain_bar));   // every MMA has finished before TMEM is released
       mbar_wait_drain(smem_u32(drain_bar), 0);
@@ -417,9 +500,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
       for (int t = 0; t < kFewRows; ++t) acc[t] = 0.0f;
       const Run first = run_at(s);
-      bool whole = false;
-      for (;;) {
+      const int t0 = first.t0, t1 = min(t0 + first.len, s1);
+      if (s > t0 + first.last) { s = t1; continue; }   // the tile's last step began in the CTA before
+      const int from = s;
+      const bool whole = from == t0 && t1 > t0 + first.last;
+      while (s < t1) {
         const Run r = run_at(s);
+        s = r.next;
+        if (r.n == 0) continue;
         const int abuf = nrun & 1;
         int ok = 1;
         if (lane == 0) ok = mbar_wait(smem_u32(acc_full + abuf), (uint32_t)(nrun >> 1 & 1), a.status, abort_flag);
@@ -431,31 +519,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(smem_u32(acc_empty + abuf));
-        if constexpr (MODE == FEW_DOWN) {
+        if (MODE == FEW_DOWN && !r.shared) {
           const int have = tokens[r.u];
 #pragma unroll
           for (int t = 0; t < kFewRows; ++t)
             if (have >> t & 1) acc[t] = fmaf(hw[r.u * a.T + t], __uint_as_float(v[t]), acc[t]);
         } else {
 #pragma unroll
-          for (int t = 0; t < kFewRows; ++t) acc[t] = __uint_as_float(v[t]);
+          for (int t = 0; t < kFewRows; ++t) acc[t] += __uint_as_float(v[t]);
         }
         ++nrun;
-        s += r.n;
-        whole = r.kk + r.n == KT;
-        if (whole || s == s1) break;
       }
-      const int tile = first.tile;
       bool finish = true;
-      if (first.kk != 0 || !whole) {
+      if (!whole) {
         // part of the tile's contraction: publish it; the last of the tile's CTAs adds them up
-        float* mine = a.part + (size_t)(2 * c + (first.kk == 0 ? 1 : 0)) * kFewPart + row;
+        float* mine = a.part + (size_t)(2 * c + (from == t0 ? 1 : 0)) * kFewPart + row;
 #pragma unroll
         for (int t = 0; t < kFewRows; ++t)
           if (t < a.T) mine[t * 256] = acc[t];
         few_bar();
-        const long long t0 = (long long)tile * KT;
-        const int c_lo = (int)(((t0 + 1) * G - 1) / total), c_hi = (int)(((t0 + KT) * G - 1) / total);   // unit = 1
+        // (unit = 1) the CTAs with the tile's first and last step
+        const int c_lo = (int)(((t0 + 1ll) * G - 1) / total), c_hi = (int)(((t0 + first.last + 1ll) * G - 1) / total);
         if (et == 0) {
           __threadfence();   // the CTA's partial, ordered before the count
           const bool last = atomicAdd(a.counters + c_lo, 1u) == (unsigned)(c_hi - c_lo);
@@ -507,7 +591,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               if (t < a.T) red[t * 128 + ch] = acc[t];
           }
           few_bar();
-          if (half == 0) {
+          if (half == 0 && first.shared) {
+            __nv_bfloat16* h = a.hsh + first.m * 128 + ch;
+#pragma unroll
+            for (int t = 0; t < kFewRows; ++t)
+              if (t < a.T) h[(size_t)t * a.sh_tiles * 128] = __float2bfloat16_rn(glu_f<ACT>(acc[t], red[t * 128 + ch]));
+          } else if (half == 0) {
             const int have = tokens[first.u];
             uint8_t* codes = a.hq + (size_t)first.u * a.T * a.m_tiles * 128 + first.m * 128 + ch;
             uint8_t* atom = a.hs + ((size_t)first.u * a.m_tiles + first.m) * 512 + q;
@@ -522,23 +611,23 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
           }
         } else {
-          const int o_row = tile * 256 + row;
+          const int o_row = first.tile * 256 + row;
           if (o_row < a.rows) {
 #pragma unroll
             for (int t = 0; t < kFewRows; ++t) {
               if (t >= a.T) break;
               const size_t o = (size_t)t * a.rows + o_row;
               if (MODE == FEW_LINEAR && a.y_f32) ((float*)a.y)[o] = acc[t];
-              else ((__nv_bfloat16*)a.y)[o] = __float2bfloat16_rn(acc[t] + (MODE == FEW_DOWN && a.ys ? a.ys[o] : 0.0f));
+              else ((__nv_bfloat16*)a.y)[o] = __float2bfloat16_rn(acc[t]);
             }
           }
         }
       }
     }
     if (MODE == FEW_DOWN && total == 0) {
-      // every id was invalid: the shared expert's output alone
+      // every id was invalid, and no shared expert
       for (size_t i = (size_t)c * 256 + et; i < (size_t)a.T * a.rows; i += (size_t)gridDim.x * 256)
-        ((__nv_bfloat16*)a.y)[i] = __float2bfloat16_rn(a.ys ? a.ys[i] : 0.0f);
+        ((__nv_bfloat16*)a.y)[i] = __float2bfloat16_rn(0.0f);
     }
   }
   __syncthreads();

@@ -257,7 +257,8 @@ def draws(T, E, k, seed):
     (1, 128, 1, 1, 128, 0, "silu"), (1, 256, 16, 4, 128, 128, "silu"), (2, 384, 8, 3, 256, 0, "clamped_swiglu"),
     (3, 512, 32, 4, 256, 0, "silu"), (5, 1152, 10, 3, 640, 384, "silu"), (8, 256, 40, 32, 128, 0, "silu"),
     (8, 640, 4, 4, 384, 256, "clamped_swiglu"), (7, 256, 300, 8, 128, 0, "silu"), (8, 1024, 64, 16, 512, 0, "silu"),
-    (16, 384, 64, 32, 256, 128, "silu"), (11, 256, 4096, 2, 128, 0, "silu")])
+    (16, 384, 64, 32, 256, 128, "silu"), (1, 1024, 4, 2, 128, 1024, "silu"), (2, 3584, 4, 1, 256, 640, "clamped_swiglu"),
+    (4, 128, 2, 1, 128, 2048, "silu"), (11, 256, 4096, 2, 128, 0, "silu")])
 def test_forward_decode(T, d, E, k, I, Is, act):
     case = Case(synth.custom(seed=T + E, T=T, d=d, E=E, k=k, I=I, I_shared=Is), act=act)
     idx, w = draws(T, E, k, 5)
