@@ -109,6 +109,11 @@ __host__ __device__ inline int few_unit(int tiles, int KT, int grid) {
   const long long total = (long long)tiles * KT;
   return (long long)((tiles + grid - 1) / grid) * KT <= (total + grid - 1) / grid + kFewSplitCost ? KT : 1;
 }
+__device__ __forceinline__ bool elect_one() {   // one lane of the converged warp, the same one each time
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void few_bar() {   // the epilogue warps
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
@@ -143,7 +148,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   float* s_w = (float*)(s_idx + slots);
   float* hw = s_w + slots;                        // [used expert][T]: the token's routing weight
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // values that the compiler cannot see are the same in a warp come through a shuffle: what depends on
+  // them then lives in uniform registers, where the MMA operands have to be
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(smem_u32(full_bar + s), 3);                          // two producers, the scale warp's commit
@@ -173,7 +180,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   // FEW_DOWN always follows FEW_GLU, which lets it start only after its own wait: all that was
   // launched before FEW_GLU is done by then, the ids, the routing weights and the packed weights
   // among it.  So its tables and weight loads begin here, and what FEW_GLU writes, and every buffer
@@ -183,13 +190,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   int used = 1;
   if constexpr (MODE != FEW_LINEAR) {
+    for (int i = tid; i < slots; i += kFewThreads) {
+      s_idx[i] = a.idx[i];
+      if (MODE == FEW_DOWN) s_w[i] = a.w[i];
+    }
     for (int i = tid; i < 128; i += kFewThreads) bitmap[i] = 0;
     for (int i = tid; i < slots; i += kFewThreads) tokens[i] = 0;
     __syncthreads();
     for (int i = tid; i < slots; i += kFewThreads) {
-      const int e = a.idx[i];
-      s_idx[i] = e;
-      if (MODE == FEW_DOWN) s_w[i] = a.w[i];
+      const int e = s_idx[i];
       if (e >= 0 && e < a.E) atomicOr(&bitmap[e >> 5], 1u << (e & 31));
       else if (blockIdx.x == 0) atomicOr(a.status, MOE_DEV_ERR_BOUNDS);   // an id outside [0, E): skipped
     }
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (lane == 31) *s_used = inc;
     }
     __syncthreads();
-    used = *s_used;
+    used = __shfl_sync(0xffffffffu, *s_used, 0);
     for (int i = tid; i < slots; i += kFewThreads) {
       const int e = s_idx[i], t = i / a.k;
       if (e < 0 || e >= a.E) continue;
@@ -413,67 +422,56 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __syncwarp();
   } else if (warp == 1 || warp == 12) {
     // ------------------------------------------------------------- MMA issuers, one per 128-row half
-    if (lane == 0) {
-      const int h = warp == 12;
-      const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, 2);
-      uint32_t idesc[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) idesc[j] = idesc_mx_e2m1_e4m3(128, kFewRows, j, j);
-      int stage = 0, nfill = 0, nrun = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int s = s0; s < s1 && ok;) {
-        const Run r = run_at(s);
-        if (r.n == 0) { s = r.next; continue; }
-        const int abuf = nrun & 1;
-        const uint32_t acc_t = tmem_base + 32 * abuf + kFewRows * h;
-        // the accumulator is free once the epilogue has drained the run before the last one
-        ok = mbar_wait(smem_u32(acc_empty + abuf), (uint32_t)(nrun >> 1 & 1) ^ 1u, a.status, abort_flag);
-        if (!ok) break;
-        // the loop is compiled once for each kind: the issue rate hangs on what this one thread executes
-        auto run_steps = [&](auto shared) {
-          auto issue_stage = [&](int st, uint32_t acc0) {
-            const uint64_t a_desc = desc0 + (uint64_t)((st * kFewStage + h * 16384) >> 4);
-            const uint64_t b_desc = desc0 + (uint64_t)((st * kFewStage + kFewATile) >> 4);
-            const uint32_t tsf = tmem_base + 64 + 16 * st;
+    // The warp runs the loop together and elects the lane that issues: in a branch of one lane the
+    // operands of every MMA would be moved to uniform registers one by one.
+    const int h = warp == 12;
+    const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, 2);
+    int stage = 0, nfill = 0, nrun = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int s = s0; s < s1 && ok;) {
+      const Run r = run_at(s);
+      s = r.next;
+      if (r.n == 0) continue;
+      const int abuf = nrun & 1;
+      const uint32_t acc_t = tmem_base + 32 * abuf + kFewRows * h;
+      // the accumulator is free once the epilogue has drained the run before the last one
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(acc_empty + abuf), (uint32_t)(nrun >> 1 & 1) ^ 1u, a.status, abort_flag));
+      if (!ok) break;
+      auto run_steps = [&](auto shared) {   // compiled once for each kind
+        for (int i = 0; i < r.n; ++i) {
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(full_bar + stage), phase, a.status, abort_flag));
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t a_desc = desc0 + (uint64_t)((stage * kFewStage + h * 16384) >> 4);
+          const uint64_t b_desc = desc0 + (uint64_t)((stage * kFewStage + kFewATile) >> 4);
+          const uint32_t tsf = tmem_base + 64 + 16 * stage;
+          if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+              const uint32_t acc = i > 0 || j > 0;
               if constexpr (decltype(shared)::value)
-                mma_bf16(acc_t, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4), idesc_bf16(128, kFewRows),
-                         j > 0 ? 1u : acc0);
+                mma_bf16(acc_t, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4), idesc_bf16(128, kFewRows), acc);
               else
-                mma_mxf8f6f4(acc_t, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4), idesc[j],
-                             (tsf + 4 * h) | ((uint32_t)j << 30), (tsf + 8) | ((uint32_t)j << 30), j > 0 ? 1u : acc0);
+                mma_mxf8f6f4(acc_t, a_desc + (uint64_t)((32 * j) >> 4), b_desc + (uint64_t)((32 * j) >> 4),
+                             idesc_mx_e2m1_e4m3(128, kFewRows, j, j), (tsf + 4 * h) | ((uint32_t)j << 30),
+                             (tsf + 8) | ((uint32_t)j << 30), acc);
             }
-          };
-          for (int i = 0; i < r.n;) {
-            const int stage2 = stage + 1 == a.stages ? 0 : stage + 1;
-            const uint32_t phase2 = stage + 1 == a.stages ? phase ^ 1u : phase;
-            ok = mbar_wait(smem_u32(full_bar + stage), phase, a.status, abort_flag);
-            if (!ok) return;
-            // a second stage in the same round where it has landed already
-            const bool two = i + 1 < r.n && mbar_try_wait(smem_u32(full_bar + stage2), phase2);
-            tc_fence_after();
-            issue_stage(stage, i > 0 ? 1u : 0u);
             tc_commit(smem_u32(empty_bar + stage));
-            if (two) {
-              issue_stage(stage2, 1u);
-              tc_commit(smem_u32(empty_bar + stage2));
-            }
-            i += two ? 2 : 1;
-            nfill += two ? 2 : 1;
-            stage = stage2;
-            phase = phase2;
-            if (two && ++stage == a.stages) { stage = 0; phase ^= 1; }
           }
-        };
-        if (MODE != FEW_LINEAR && r.shared) run_steps(std::true_type{});
-        else run_steps(std::false_type{});
-        if (!ok) break;
-        tc_commit(smem_u32(acc_full + abuf));
-        ++nrun;
-        s = r.next;
-      }
+          __syncwarp();
+          ++nfill;
+          if (++stage == a.stages) { stage = 0; phase ^= 1; }
+        }
+      };
+      if (MODE != FEW_LINEAR && r.shared) run_steps(std::true_type{});
+      else run_steps(std::false_type{});
+      if (!ok) break;
+      if (elect_one()) tc_commit(smem_u32(acc_full + abuf));
+      __syncwarp();
+      ++nrun;
+    }
+    if (elect_one()) {
       tc_commit(smem_u32(drain_bar));   // every MMA has finished before TMEM is released
       mbar_wait_drain(smem_u32(drain_bar), 0);
       fills[3 + h] = nfill;
