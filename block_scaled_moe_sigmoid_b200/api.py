@@ -109,7 +109,7 @@ def lib():
 
 
 def _call(name, *args):
-    code = getattr(lib(), name)(*args)
+    code = getattr(_lib or lib(), name)(*args)
     if code != MOE_OK:
         raise MoeError(name, code)
 
@@ -335,16 +335,28 @@ def moe_add_rmsnorm_mxfp8(x, gamma, eps=1e-5, residual=None, residual_out=None, 
         rtype, pr = _type("residual", residual.dtype), _checked("residual", residual, residual.dtype, shape, i)
         if residual_out is None:
             residual_out = torch.empty_like(residual)
-        pro = _checked("residual_out", residual_out, residual.dtype, shape, i)
+            pro = residual_out.data_ptr()
+        else:
+            pro = _checked("residual_out", residual_out, residual.dtype, shape, i)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if with_xn:
-        xn = torch.empty_like(x) if xn is None else xn
-        pn = _checked("xn", xn, torch.bfloat16, shape, i)
+        if xn is None:
+            xn = torch.empty_like(x)
+            pn = xn.data_ptr()
+        else:
+            pn = _checked("xn", xn, torch.bfloat16, shape, i)
     if with_mx:
-        q = torch.empty_like(x, dtype=torch.uint8) if q is None else q
-        scale = torch.empty_strided(blocks, (blocks[1], 1), dtype=torch.uint8, device=x.device) if scale is None else scale
-        pq, ps = _checked("q", q, torch.uint8, shape, i), _checked("scale", scale, torch.uint8, blocks, i)
+        if q is None:
+            q = torch.empty_like(x, dtype=torch.uint8)
+            pq = q.data_ptr()
+        else:
+            pq = _checked("q", q, torch.uint8, shape, i)
+        if scale is None:
+            scale = torch.empty_strided(blocks, (blocks[1], 1), dtype=torch.uint8, device=x.device)
+            ps = scale.data_ptr()
+        else:
+            ps = _checked("scale", scale, torch.uint8, blocks, i)
     _call("moe_add_rmsnorm_mxfp8", px, pr, rtype, _checked("gamma", gamma, torch.float32, (cols,), i), eps, rows, cols, pro,
           pn, pq, ps, _raw_stream(i))
     return residual_out, xn, q, scale

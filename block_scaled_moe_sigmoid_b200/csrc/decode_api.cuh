@@ -11,6 +11,13 @@ bool make_few_maps(CUtensorMap* mW, CUtensorMap* mX, const void* w, uint64_t til
          make_map(mX, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, K, rows, K, 128, kFewRows);
 }
 
+// Pipeline stages that fit next to few_kernel's tables; it wants three at least.
+int few_stages(int mode, int T, int k, int k_tiles) {
+  const long long fixed = few_smem(mode, T, k, k_tiles, 0).total;
+  return (int)std::min<long long>(kFewMaxStages, (kFewSmemMax - fixed) / (kFewStage + kFewSF));
+}
+constexpr int kFewMinStages = 3;
+
 // Launch few_kernel with as many pipeline stages as fit.
 template <int MODE, int ACT>
 cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, const CUtensorMap& tX, const CUtensorMap& tSW, const CUtensorMap& tSX,
@@ -19,9 +26,8 @@ cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, const CUtensorMap& tX, 
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_attr(kern, kFewSmemMax, done);
   if (e != cudaSuccess) return e;
-  const int fixed = few_smem(MODE, a.T, a.k, a.k_tiles, 0).total;
-  a.stages = std::min(kFewMaxStages, (kFewSmemMax - fixed) / (kFewStage + kFewSF));
-  if (a.stages < 3) return cudaErrorInvalidValue;
+  a.stages = few_stages(MODE, a.T, a.k, a.k_tiles);
+  if (a.stages < kFewMinStages) return cudaErrorInvalidValue;   // the callers check before any launch
   return launch_k(kern, grid, kFewThreads, few_smem(MODE, a.T, a.k, a.k_tiles, a.stages).total, s, a, tW, tX, tSW, tSX);
 }
 
@@ -109,7 +115,7 @@ moe_status_t moe_linear_create(int T_max, int N, int K, moe_linear_t* out) {
   if (T_max < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
   const long long m_tiles = ((long long)N + 255) / 256;
   // tensor-map coordinates are 32-bit: tile rows of the weights, and token rows
-  if (K % 128 || m_tiles * (K / 128) * 256 > (1ll << 30) || T_max > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (K % 128 || K > (1 << 22) || m_tiles * (K / 128) * 256 > (1ll << 30) || T_max > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   moe_linear_s* p = new moe_linear_s();
   p->T_max = T_max; p->N = N; p->K = K;
   int dev = 0, sms = 0;
@@ -203,7 +209,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
   if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
   cudaStream_t s = S(stream);
   const int N = p->N, K = p->K, k_tiles = K / 128, m_tiles = (N + 255) / 256;
-  if (T <= kFewRows) {
+  if (T <= kFewRows && few_stages(FEW_LINEAR, T, 0, k_tiles) >= kFewMinStages) {
     CUtensorMap tW, tX;
     if (!make_few_maps(&tW, &tX, W->w, (uint64_t)m_tiles * k_tiles, q, T, K)) return MOE_ERR_CUDA;
     FewArgs a;
@@ -225,7 +231,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
   // more rows: the block-scaled GEMM on one dense group
   const int bn = moe_linear_s::tile_rows(T), nt = (T + bn - 1) / bn;
   uint8_t* xs = p->at<uint8_t>(p->o_xs);
-  if (launch_k(linear_scale_tiles_kernel, dim3(nt, std::min(k_tiles, 8)), 256, 0, s, scale, T, bn, k_tiles, xs) != cudaSuccess)
+  if (launch_k(linear_scale_tiles_kernel, dim3(nt, k_tiles), 256, 0, s, scale, T, bn, k_tiles, xs) != cudaSuccess)
     return MOE_ERR_CUDA;
   CUtensorMap tA;
   BMaps tB;
@@ -263,11 +269,13 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
     e = launch_linear_gemm<EPI_F32>(bn, a, tA, tB, grid, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     const long long n = (long long)T * N;
-    if (y_type == MOE_TYPE_F32)
-      e = launch_k(split_sum_kernel, (unsigned)((n + 255) / 256), 256, 0, s, part, ks, n, a.split_stride, (float*)y);
-    else
-      e = launch_k(split_sum_bf16_kernel, (unsigned)((n + 255) / 256), 256, 0, s, part, ks, n, a.split_stride,
-                   (__nv_bfloat16*)y);
+    auto sum = [&](auto kern4, auto kern1, auto* out) {
+      const int v = n % 4 ? 1 : 4;
+      const unsigned blocks = (unsigned)((n / v + 255) / 256);
+      e = v == 4 ? launch_k(kern4, blocks, 256, 0, s, part, ks, n, out) : launch_k(kern1, blocks, 256, 0, s, part, ks, n, out);
+    };
+    if (y_type == MOE_TYPE_F32) sum(linear_split_sum_kernel<float, 4>, linear_split_sum_kernel<float, 1>, (float*)y);
+    else sum(linear_split_sum_kernel<__nv_bfloat16, 4>, linear_split_sum_kernel<__nv_bfloat16, 1>, (__nv_bfloat16*)y);
   } else if (y_type == MOE_TYPE_F32) {
     e = launch_linear_gemm<EPI_F32>(bn, a, tA, tB, grid, s);
   } else {
@@ -281,7 +289,9 @@ moe_status_t moe_forward_decode(moe_plan_t p, const void* x, const uint8_t* q, c
                                 const int32_t* idx, const float* w, const moe_experts_mxfp4* ex,
                                 const moe_shared_bf16* sh, void* y, void* stream) {
   if (!p || T < 0 || p->dl > 0) return MOE_ERR_INVALID_ARG;   // no latent form
-  if (T > p->T_max || T > kFewRows) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T > p->T_max || T > kFewRows || few_stages(FEW_GLU, T, p->k, p->d / 128) < kFewMinStages ||
+      few_stages(FEW_DOWN, T, p->k, p->I / 128) < kFewMinStages)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
   if ((q != nullptr) != (scale != nullptr) || (!x && (!q || p->Is > 0))) return MOE_ERR_INVALID_ARG;
   if (!idx || !w || !ex || !y || !ex->w_gu || !ex->s_gu || !ex->w_dn || !ex->s_dn) return MOE_ERR_INVALID_ARG;

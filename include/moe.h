@@ -285,7 +285,7 @@ moe_status_t moe_add_rmsnorm_mxfp8(const void* x_bf16, const void* residual, moe
  * a stream of the weights over all SMs, more rows on the tensor cores' block-scaled GEMM; both
  * read the same packed weights.
  * moe_linear_create: a host object for calls of up to T_max rows on matrices of one shape;
- * N >= 1, K % 128 == 0, and at most 2^30 / 256 tiles of 256 x 128.  Workspace, check and destroy
+ * N >= 1, K % 128 == 0, K <= 2^22, and at most 2^30 / 256 tiles of 256 x 128.  Workspace, check and destroy
  * as for moe_plan_*: caller-owned device memory, one call at a time per object. */
 typedef struct moe_linear_s* moe_linear_t;
 /* A packed matrix (device pointers; w 256-byte, s 16-byte aligned), in the tile-major layout of
@@ -319,7 +319,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t linear, const uint8_t* q_e4m3, const 
  * [T][d/32], the MXFP8 form of the tokens (moe_add_rmsnorm_mxfp8, moe_quant_mxfp8), or both NULL.
  * Other arguments as moe_forward.  An id outside [0, E) contributes nothing and is flagged
  * (MOE_ERR_DEVICE_FAULT at moe_plan_check); an expert that a token names twice counts with the
- * sum of both weights.  T <= 16; not for latent plans (MOE_ERR_INVALID_ARG).  Uses the
+ * sum of both weights.  T <= 16 (and d up to 200,000); not for latent plans (MOE_ERR_INVALID_ARG).  Uses the
  * plan workspace (one call at a time per plan). */
 moe_status_t moe_forward_decode(moe_plan_t plan, const void* x_bf16, const uint8_t* q_e4m3,
                                 const uint8_t* scale_e8m0, int T, const int32_t* idx, const float* w,

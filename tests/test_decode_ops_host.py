@@ -36,7 +36,7 @@ def test_norm_refusals(kw, code):
 def test_linear_create_and_size_refusals():
     L, h = api.lib(), P()
     for args, code in (((-1, 8, 128), INVALID), ((8, 0, 128), INVALID), ((8, 8, 0), INVALID), ((8, 8, 96), SHAPE),
-                       ((8, 1 << 30, 1 << 15), SHAPE), (((1 << 30) + 1, 8, 128), SHAPE)):
+                       ((8, 1 << 30, 1 << 15), SHAPE), ((8, 8, (1 << 22) + 128), SHAPE), (((1 << 30) + 1, 8, 128), SHAPE)):
         assert L.moe_linear_create(*args, ctypes.byref(h)) == code, args
         assert not h
     assert L.moe_linear_create(8, 8, 128, None) == INVALID
