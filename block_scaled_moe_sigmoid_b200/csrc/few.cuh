@@ -177,26 +177,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     tmem_alloc(smem_u32(tmem_holder), kFewTmemCols);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   // FEW_DOWN always follows FEW_GLU, which lets it start only after its own wait: all that was
   // launched before FEW_GLU is done by then, the ids, the routing weights and the packed weights
   // among it.  So its tables and weight loads begin here, and what FEW_GLU writes, and every buffer
   // that it shares with it, waits (token producer, epilogue).
   if (MODE != FEW_DOWN) griddep_wait();
   griddep_launch_dependents();
-
-  int used = 1;
+  // loads that the first barrier covers: the ids, or the token scales
   if constexpr (MODE != FEW_LINEAR) {
     for (int i = tid; i < slots; i += kFewThreads) {
       s_idx[i] = a.idx[i];
-      if (MODE == FEW_DOWN) s_w[i] = a.w[i];
+      tokens[i] = 0;
     }
     for (int i = tid; i < 128; i += kFewThreads) bitmap[i] = 0;
-    for (int i = tid; i < slots; i += kFewThreads) tokens[i] = 0;
-    __syncthreads();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+
+  int used = 1;
+  if constexpr (MODE != FEW_LINEAR) {
     for (int i = tid; i < slots; i += kFewThreads) {
       const int e = s_idx[i];
       if (e >= 0 && e < a.E) atomicOr(&bitmap[e >> 5], 1u << (e & 31));
@@ -220,18 +221,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __syncthreads();
     used = __shfl_sync(0xffffffffu, *s_used, 0);
     for (int i = tid; i < slots; i += kFewThreads) {
-      const int e = s_idx[i], t = i / a.k;
+      const int e = s_idx[i];
       if (e < 0 || e >= a.E) continue;
       const int u = prefix[e >> 5] + __popc(bitmap[e >> 5] & ((1u << (e & 31)) - 1u));
       elist[u] = e;
-      atomicOr(&tokens[u], 1 << t);
-      if constexpr (MODE == FEW_DOWN) {
-        // an expert that a token names twice counts with the sum of both weights, in slot order
-        float w = 0.0f;
-        for (int j = 0; j < a.k; ++j)
-          if (s_idx[t * a.k + j] == e) w += s_w[t * a.k + j];
-        hw[u * a.T + t] = w;
-      }
+      atomicOr(&tokens[u], 1 << (i / a.k));
     }
     __syncthreads();
   }
@@ -485,6 +479,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int et = tid - 64;   // 0 .. 255
     float* red = (float*)(smem + L.red);
     if constexpr (MODE == FEW_DOWN) {
+      // the tokens' weights, while the first steps load; an expert that a token names twice counts
+      // with the sum of both, in slot order
+      for (int i = et; i < slots; i += 256) s_w[i] = a.w[i];
+      few_bar();
+      for (int i = et; i < used * a.T; i += 256) {
+        const int e = elist[i / a.T], t = i % a.T;
+        float w = 0.0f;
+        for (int j = 0; j < a.k; ++j)
+          if (s_idx[t * a.k + j] == e) w += s_w[t * a.k + j];
+        hw[i] = w;
+      }
+      few_bar();
       griddep_wait();
     } else {
       uint32_t* xs = (uint32_t*)(smem + L.xs);
