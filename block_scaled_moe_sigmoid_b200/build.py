@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_sm100.so")
 SOURCES = ["api.cu"]
-DEPS = ["api.cu", "decode_api.cuh", "few.cuh", "gemm.cuh", "gemm_pair.cuh", "kernels.cuh", "norm.cuh", "ptx.cuh", "router.cuh",
+DEPS = ["api.cu", "decode_api.cuh", "few.cuh", "gemm.cuh", "gemm_pair.cuh", "kernels.cuh", "linear.cuh", "norm.cuh", "ptx.cuh", "router.cuh",
         "tiling.cuh"]
 HEADER = os.path.join(os.path.dirname(HERE), "include", "moe.h")
 

@@ -14,6 +14,7 @@
 #include "gemm_pair.cuh"
 #include "few.cuh"
 #include "kernels.cuh"
+#include "linear.cuh"
 #include "norm.cuh"
 #include "router.cuh"
 

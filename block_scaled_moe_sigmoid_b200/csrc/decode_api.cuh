@@ -31,11 +31,16 @@ cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, const CUtensorMap& tX, 
   return launch_k(kern, grid, kFewThreads, few_smem(MODE, a.T, a.k, a.k_tiles, a.stages).total, s, a, tW, tX, tSW, tSX);
 }
 
-// The dense block-scaled GEMM in its two token-tile configurations.
-template <int EPI>
-cudaError_t launch_linear_gemm(int bn, const GemmArgs& a, const CUtensorMap& tA, const BMaps& tB, int grid, cudaStream_t s) {
-  if (bn == kBNSmall) return launch_gemm_cfg<KIND_MX, EPI, kBNSmall, kStagesSmall>(a, tA, tB, grid, s);
-  return launch_gemm_cfg<KIND_MX, EPI, kBN, kStages>(a, tA, tB, grid, s);
+template <int NB>
+cudaError_t launch_linear(const LinearArgs& a, const CUtensorMap& tW, const CUtensorMap& tX, cudaStream_t s) {
+  auto kern = linear_kernel<NB>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = ensure_smem_attr(kern, LinearCfg<NB>::SMEM, done);
+  if (e != cudaSuccess) return e;
+  e = launch_k(kern, a.ctas, kLinearThreads, LinearCfg<NB>::SMEM, s, a, tW, tX);
+  if (e == cudaSuccess && a.unit < a.k_tiles)
+    e = launch_k(linear_sum_kernel, dim3(a.n_tiles * a.m_tiles, a.n_per / 4), 256, 0, s, a);
+  return e;
 }
 
 // The norm's variants.  A thread holds V vectors of 8 elements: one where a row fits 1024 threads so,
@@ -75,12 +80,40 @@ struct moe_linear_s {
   int T_max, N, K;
   int num_sms = 148;
   char* ws = nullptr;
-  size_t o_status, o_cnt, o_part, o_xs, o_split, split_floats, total;
+  size_t o_status, o_cnt, o_part, total;
+  int grid() const { return std::min(num_sms, kFewMaxCtas); }
   template <class P>
   P* at(size_t off) const { return (P*)(ws + off); }
-  // token rows per tile of the GEMM path
-  static int tile_rows(int T) { return T <= 64 ? kBNSmall : kBN; }
 };
+// linear_kernel's tiles: up to 64 token rows with five pipeline stages, or up to 176 (the widest whose
+// accumulators, with four stages' scales, fit the tensor memory and whose stages fit shared memory).
+constexpr int kLinearSmall = 64, kLinearWide = 176, kLinearMany = 1024;
+
+// Token rows per tile (a multiple of 16) and whether tiles stay whole, by the time each choice takes, in
+// ns, fitted to 7168 x 7168, 7168 x 1024, 1003 x 7168 and 40000 x 7168 with 32 to 1024 rows:
+//   a step of n rows takes 255 + 0.77 n (n <= 64) or 190 + 2.1 n: up to 64 rows the issue and the weights,
+//   above them the shared memory's fill rate;
+//   exchanging partials takes 2500 + 55 n, and whole tiles the last wave's idle SMs.
+// 300 rows of 7168 x 7168: five whole tiles of 64 rows by 28 take 20.9 us, two of 160 split 27.3; 64 rows:
+// one tile split 13.2, two whole ones 19.5.  Past 1024 rows wide whole tiles win for their fewer loads
+// (2048 rows: 176 100 us, 112 115, 64 139).
+struct LinearPick { int n_per, unit; };
+LinearPick pick_linear_tiles(int T, int m_tiles, int k_tiles, int grid) {
+  if (T > kLinearMany) return {kLinearWide, k_tiles};
+  LinearPick best = {kLinearWide, k_tiles};
+  double best_ns = 1e30;
+  for (int n = 16; n <= kLinearWide; n += 16) {
+    const long long tiles = (long long)((T + n - 1) / n) * m_tiles, steps = tiles * k_tiles;
+    const double step = n <= kLinearSmall ? 255.0 + 0.77 * n : 190.0 + 2.1 * n;
+    const double whole = (double)((tiles + grid - 1) / grid) * k_tiles * step;
+    const long long ctas = std::max(std::min(steps / 4, (long long)grid), 1ll);
+    const double split = (double)((steps + ctas - 1) / ctas) * step + 2500.0 + 55.0 * n;
+    if (whole < best_ns) { best_ns = whole; best = {n, k_tiles}; }
+    if (k_tiles > 1 && split < best_ns) { best_ns = split; best = {n, 1}; }
+    if (n >= T) break;
+  }
+  return best;
+}
 
 extern "C" {
 
@@ -126,12 +159,8 @@ moe_status_t moe_linear_create(int T_max, int N, int K, moe_linear_t* out) {
   auto take = [&](size_t bytes) { size_t r = o; o = up(o + bytes, 1024); return r; };
   p->o_status = take(256);
   p->o_cnt = take((size_t)kFewMaxCtas * 4);
-  p->o_part = take((size_t)2 * kFewMaxCtas * kFewPart * 4);
-  // GEMM path: token scale blocks, and the partials of a split K (at most kSplitMaxCtas tiles of
-  // at most kBN x 256, and no more splits than K / 512)
-  p->o_xs = take(((size_t)T_max / kBNMin + 2) * (K / 128) * SF_TILE_BYTES);
-  p->split_floats = std::min((size_t)kSplitMaxCtas * kBN * 256, (size_t)(K / 512) * T_max * N);
-  p->o_split = take(p->split_floats * 4);
+  // fp32 partials of two ragged tiles per CTA
+  p->o_part = take((size_t)2 * p->grid() * std::min(std::max((T_max + 15) / 16 * 16, 16), kLinearWide) * 256 * 4);
   p->total = o;
   *out = p;
   return MOE_OK;
@@ -225,62 +254,37 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
     a.part = p->at<float>(p->o_part);
     a.counters = p->at<unsigned int>(p->o_cnt);
     a.status = p->at<unsigned int>(p->o_status);
-    const int grid = std::min(m_tiles * k_tiles, std::min(p->num_sms, kFewMaxCtas));
+    const int grid = std::min(m_tiles * k_tiles, p->grid());
     return launch_few<FEW_LINEAR, 0>(a, tW, tX, tW, tX, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
-  // more rows: the block-scaled GEMM on one dense group
-  const int bn = moe_linear_s::tile_rows(T), nt = (T + bn - 1) / bn;
-  uint8_t* xs = p->at<uint8_t>(p->o_xs);
-  if (launch_k(linear_scale_tiles_kernel, dim3(nt, k_tiles), 256, 0, s, scale, T, bn, k_tiles, xs) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  CUtensorMap tA;
-  BMaps tB;
-  if (!make_map(&tA, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, W->w, 128, (uint64_t)m_tiles * k_tiles * 256, 64, 128, 256) ||
-      !make_bmaps(&tB, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, T, K, 128))
-    return MOE_ERR_CUDA;
-  GemmArgs a;
+  // more rows: tiles of up to 64 or 176 of them
+  const LinearPick pick = pick_linear_tiles(T, m_tiles, k_tiles, p->grid());
+  const int n_per = pick.n_per, n_tiles = (T + n_per - 1) / n_per;
+  if ((long long)n_tiles * m_tiles * k_tiles > 0x7fffffffll || (long long)n_tiles * m_tiles > 0x7fffffffll)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  LinearArgs a;
   memset(&a, 0, sizeof(a));
-  a.status = p->at<unsigned int>(p->o_status);
-  a.ksplit = 1;
-  a.dense_rows = T;
-  a.num_groups = 1;
-  a.M_total = N;
+  a.T = T;
+  a.n_per = n_per;
+  a.n_tiles = n_tiles;
   a.m_tiles = m_tiles;
   a.k_tiles = k_tiles;
-  a.kb_wrap = k_tiles;
-  a.B_rows = T;
-  a.sfa = (const uint8_t*)W->s;
-  a.a_ptr = (const uint8_t*)W->w;
-  a.sfb = xs;
-  a.out0 = y;
-  a.ld_out = N;
-  const long long tiles = (long long)nt * m_tiles;
-  if (tiles > 0x7fffffffll) return MOE_ERR_UNSUPPORTED_SHAPE;
-  int ks = tiles > kSplitMaxCtas ? 1 : dense_ksplit(p->num_sms, (int)tiles, k_tiles, (size_t)T * N);
-  if ((size_t)ks * T * N > p->split_floats) ks = 1;
-  const int grid = (int)std::min<long long>(tiles * ks, p->num_sms);
-  cudaError_t e;
-  if (ks > 1) {
-    a.ksplit = ks;
-    a.k_per = (k_tiles + ks - 1) / ks;
-    a.split_stride = (long long)T * N;
-    float* part = p->at<float>(p->o_split);
-    a.out0 = part;
-    e = launch_linear_gemm<EPI_F32>(bn, a, tA, tB, grid, s);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
-    const long long n = (long long)T * N;
-    auto sum = [&](auto kern4, auto kern1, auto* out) {
-      const int v = n % 4 ? 1 : 4;
-      const unsigned blocks = (unsigned)((n / v + 255) / 256);
-      e = v == 4 ? launch_k(kern4, blocks, 256, 0, s, part, ks, n, out) : launch_k(kern1, blocks, 256, 0, s, part, ks, n, out);
-    };
-    if (y_type == MOE_TYPE_F32) sum(linear_split_sum_kernel<float, 4>, linear_split_sum_kernel<float, 1>, (float*)y);
-    else sum(linear_split_sum_kernel<__nv_bfloat16, 4>, linear_split_sum_kernel<__nv_bfloat16, 1>, (__nv_bfloat16*)y);
-  } else if (y_type == MOE_TYPE_F32) {
-    e = launch_linear_gemm<EPI_F32>(bn, a, tA, tB, grid, s);
-  } else {
-    e = launch_linear_gemm<EPI_BF16>(bn, a, tA, tB, grid, s);
-  }
+  a.N = N;
+  a.unit = pick.unit;
+  const int units = n_tiles * m_tiles * k_tiles / a.unit;
+  a.ctas = std::min(a.unit == k_tiles ? units : std::max(units / 4, 1), p->grid());
+  a.sf = (const uint8_t*)W->s;
+  a.xs = scale;
+  a.y = y;
+  a.y_f32 = y_type == MOE_TYPE_F32;
+  a.part = p->at<float>(p->o_part);
+  a.status = p->at<unsigned int>(p->o_status);
+  CUtensorMap tW, tX;
+  if (!make_map(&tW, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, W->w, 128, (uint64_t)m_tiles * k_tiles * 256, 64, 128, 256) ||
+      !make_map(&tX, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, T, K, 128, n_per))
+    return MOE_ERR_CUDA;
+  const cudaError_t e = n_per <= kLinearSmall ? launch_linear<kLinearSmall>(a, tW, tX, s)
+                                           : launch_linear<kLinearWide>(a, tW, tX, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

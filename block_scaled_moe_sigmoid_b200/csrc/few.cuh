@@ -99,6 +99,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
+__device__ __forceinline__ unsigned int count_acq_rel(unsigned int* counter) {
+  unsigned int v;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(counter) : "memory");
+  return v;
+}
 // Order this thread's shared-memory writes before later asynchronous-proxy reads (tcgen05.cp).
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Steps that stay together in a CTA: a whole tile, or one step.  Split tiles cost the exchange of
@@ -545,42 +550,35 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         // (unit = 1) the CTAs with the tile's first and last step
         const int c_lo = (int)(((t0 + 1ll) * G - 1) / total), c_hi = (int)(((t0 + first.last + 1ll) * G - 1) / total);
         if (et == 0) {
-          __threadfence();   // the CTA's partial, ordered before the count
-          const bool last = atomicAdd(a.counters + c_lo, 1u) == (unsigned)(c_hi - c_lo);
+          // the CTA's partial ordered before the count, the others' partials after it
+          const bool last = count_acq_rel(a.counters + c_lo) == (unsigned)(c_hi - c_lo);
           if (last) a.counters[c_lo] = 0;
-          __threadfence();
           *s_last = last;
         }
         few_bar();
         finish = *s_last;
         if (finish) {
-          // four tokens and four CTAs at a time, so that the loads overlap (rows past T are loaded,
+          // eight tokens and four CTAs at a time, so that the loads overlap (rows past T are loaded,
           // never used)
 #pragma unroll
-          for (int t4 = 0; t4 < kFewRows; t4 += 4) {
-            if (t4 >= a.T) break;
-            const float* p = a.part + (size_t)(2 * c_lo + 1) * kFewPart + t4 * 256 + row;
-            float v[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) v[t] = __ldcg(p + t * 256);
-            p = a.part + (size_t)(2 * c_lo + 2) * kFewPart + t4 * 256 + row;
-            int i = c_lo + 1;
-            for (; i + 3 <= c_hi; i += 4, p += 8 * kFewPart) {
-              float n[4][4];
+          for (int t8 = 0; t8 < kFewRows; t8 += 8) {
+            if (t8 >= a.T) break;
+            const float* p = a.part + (size_t)(2 * c_lo) * kFewPart + t8 * 256 + row;
+            float v[8] = {};
+            for (int i = c_lo; i <= c_hi; i += 4, p += 8 * kFewPart) {
+              float n[4][8];
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) n[j][t] = __ldcg(p + j * 2 * kFewPart + t * 256);
+                for (int t = 0; t < 8; ++t)
+                  n[j][t] = i + j <= c_hi ? __ldcg(p + (2 * j + (i + j == c_lo ? 1 : 0)) * kFewPart + t * 256) : 0.0f;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) v[t] += n[j][t];
+                for (int t = 0; t < 8; ++t) v[t] += n[j][t];
             }
-            for (; i <= c_hi; ++i, p += 2 * kFewPart)
 #pragma unroll
-              for (int t = 0; t < 4; ++t) v[t] += __ldcg(p + t * 256);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc[t4 + t] = v[t];
+            for (int t = 0; t < 8; ++t) acc[t8 + t] = v[t];
           }
         }
       }
@@ -646,55 +644,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, kFewTmemCols);
-  }
-}
-
-// Token-side scale blocks of the dense block-scaled GEMM, tile-major (tiling.cuh): one CTA per
-// group-tile and K tile, one thread per row of its scale atoms.
-__global__ void __launch_bounds__(256)
-    linear_scale_tiles_kernel(const uint8_t* __restrict__ xs, int rows, int bn, int k_tiles, uint8_t* __restrict__ out) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int gt = blockIdx.x, ntiles = (rows + bn - 1) / bn;
-  const int n_per = tile_rows_per(rows, ntiles);
-  const int n_valid = min(n_per, rows - gt * n_per);
-  const int n = threadIdx.x;
-  if (n_valid <= 0 || n >= ((((n_valid + 15) & ~15) + 127) >> 7) * 128) return;
-  const bool valid = n < n_valid;
-  const uint8_t* src = xs + (valid ? (size_t)(gt * n_per + n) * k_tiles * 4 : 0);
-  uint8_t* dst = out + (size_t)gt * k_tiles * SF_TILE_BYTES + sf_atom_offset(n);
-  const int kt = blockIdx.y;
-  *(uint32_t*)(dst + (size_t)kt * SF_TILE_BYTES) = valid ? __ldg((const uint32_t*)(src + kt * 4)) : 0u;
-}
-
-// y[i] = sum over s, in order, of part[s * n + i], as bf16 or fp32: V elements per thread (one where n is
-// not a multiple of 4).  300 x 7168 in two splits, 21 MB through L2: 12 us with one element per thread.
-template <typename OUT, int V>
-__global__ void __launch_bounds__(256) linear_split_sum_kernel(const float* __restrict__ part, int nsplit, long long n,
-                                                               OUT* __restrict__ y) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * V;
-  if (i >= n) return;
-  float v[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) v[j] = 0.0f;
-  for (int s = 0; s < nsplit; ++s) {
-    if constexpr (V == 4) {
-      const float4 p = __ldcg((const float4*)(part + s * n + i));
-      v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
-    } else {
-      v[0] += __ldcg(part + s * n + i);
-    }
-  }
-  if constexpr (V == 1) {
-    if constexpr (sizeof(OUT) == 4) y[i] = v[0];
-    else y[i] = __float2bfloat16_rn(v[0]);
-  } else if constexpr (sizeof(OUT) == 4) {
-    *(float4*)(y + i) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-    *(uint2*)(y + i) = make_uint2(*(const uint32_t*)&lo, *(const uint32_t*)&hi);
   }
 }
 

@@ -158,6 +158,22 @@ def test_linear(T, N, K, dtype):
     assert torch.equal(plan.forward(q, s, lin, dtype=dtype), y)      # a fixed order of sums
 
 
+@pytest.mark.parametrize("T", [1, 8, 16, 17, 40, 64, 65, 130, 300, 520])
+def test_linear_stays_inside_its_workspace(T):
+    """Wide enough to be split over all SMs: right, and nothing written behind the workspace's bytes."""
+    N, K = 4096, 4096
+    q, s, lin, w = linear_case(T, N, K, T)
+    plan = api.LinearPlan(T, N, K)
+    need = api.moe_linear_workspace_bytes(plan.handle)
+    ws = torch.full((need + (64 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    api.moe_linear_set_workspace(plan.handle, ws[:need])
+    y = plan.forward(q, s, lin, dtype=torch.float32)
+    assert plan.check()[0] == 0
+    assert bool((ws[need:] == 0x5A).all())
+    check_linear(q, s, w, y)
+    assert torch.equal(plan.forward(q, s, lin, dtype=torch.float32), y)
+
+
 def test_linear_rows_do_not_depend_on_the_batch():
     """A row's result on the weight stream is the same alone and among seven others."""
     N, K = 777, 896
@@ -362,6 +378,21 @@ def test_forward_decode_graph_replay_and_calls_in_between():
         r_idx, r_w = case.plan.route(case.x, case.W_r, case.bias)
         case.plan.forward(case.x, r_idx, r_w, case.experts, case.shared)
     assert case.plan.check()[0] == 0
+
+
+@pytest.mark.parametrize("T", [1, 9, 16])
+def test_forward_decode_stays_inside_its_workspace(T):
+    d, E, k, I, Is = 1024, 24, 6, 512, 512
+    case = Case(synth.custom(seed=T, T=T, d=d, E=E, k=k, I=I, I_shared=Is))
+    idx, w = draws(T, E, k, 4)
+    plan = api.Plan(T, d, E, k, I, Is)
+    need = api.moe_plan_workspace_bytes(plan.handle)
+    ws = torch.full((need + (32 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    api.moe_plan_set_workspace(plan.handle, ws[:need])
+    y = plan.forward_decode(case.x, idx, w, case.experts, case.shared)
+    assert plan.check()[0] == 0
+    assert bool((ws[need:] == 0x5A).all())
+    check_decode(case, idx, w, y)
 
 
 def test_forward_decode_writes_its_rows_only():
