@@ -207,38 +207,57 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
     __syncwarp();
   } else if (warp == 13) {
     // ------------------------------------------------------------- token scales
-    // Each step's scale atoms, a word per token row (its four blocks of the K tile), from words loaded a
-    // step ahead.  (In the warp above, the stores would hold up the copies: 512 rows 34 us, not 28.)
+    // Each step's scale atoms, a word per token row (its four blocks of the K tile).  (In the warp above,
+    // the stores would hold up the copies: 512 rows 34 us, not 28.)  A row's words of four K tiles are
+    // loaded together, four steps ahead, where their 16 bytes are aligned: word by word the gather fetched
+    // a sector per row and step.
     constexpr int WORDS = (NB + 31) / 32;
-    const uint32_t* xs = (const uint32_t*)a.xs;
-    uint32_t next[WORDS];
-    auto fetch = [&](const Run& r, int kt) {
+    const bool quads = KT % 4 == 0 && ((uintptr_t)a.xs & 15) == 0;
+    uint4 cur[WORDS], next[WORDS];
+    auto fetch = [&](uint4 (&q)[WORDS], const Run& r, int kt) {
 #pragma unroll
       for (int w = 0; w < WORDS; ++w) {
         const int n = lane + 32 * w, t = r.nt * a.n_per + n;
-        next[w] = n < a.n_per && t < a.T ? __ldg(xs + (size_t)t * KT + kt) : 0u;
+        q[w] = make_uint4(0u, 0u, 0u, 0u);
+        if (n < a.n_per && t < a.T) {
+          const uint32_t* src = (const uint32_t*)a.xs + (size_t)t * KT + kt;
+          if (quads) {
+            q[w] = __ldg((const uint4*)src);
+          } else {
+            q[w].x = __ldg(src);
+            if (kt + 1 < KT) q[w].y = __ldg(src + 1);
+            if (kt + 2 < KT) q[w].z = __ldg(src + 2);
+            if (kt + 3 < KT) q[w].w = __ldg(src + 3);
+          }
+        }
       }
     };
     int stage = 0, nfill = 0;
     uint32_t phase = 0;
     bool ok = true;
-    if (s0 < s1) fetch(run_at(s0), run_at(s0).kb);
     for (int s = s0; s < s1 && ok;) {
       const Run r = run_at(s);
-      for (int i = 0; i < r.n; ++i, ++s) {
+      fetch(next, r, r.kb & ~3);
+      for (int kt = r.kb; kt < r.kb + r.n; ++kt) {
+        if (kt == r.kb || (kt & 3) == 0) {
+#pragma unroll
+          for (int w = 0; w < WORDS; ++w) cur[w] = next[w];
+          if ((kt & ~3) + 4 < r.kb + r.n) fetch(next, r, (kt & ~3) + 4);
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, a.status, abort_flag));
         if (!ok) break;
         uint8_t* atom = sf + stage * C::SF + 1024;
+        const int j = kt & 3;
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) *(uint32_t*)(atom + sf_atom_offset(lane + 32 * w)) = next[w];
+        for (int w = 0; w < WORDS; ++w)
+          *(uint32_t*)(atom + sf_atom_offset(lane + 32 * w)) = j < 2 ? (j == 0 ? cur[w].x : cur[w].y) : (j == 2 ? cur[w].z : cur[w].w);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(sf_full + stage));
-        if (i + 1 < r.n) fetch(r, r.kb + i + 1);
-        else if (s + 1 < s1) fetch(run_at(s + 1), run_at(s + 1).kb);
         ++nfill;
         if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
+      s += r.n;
     }
     if (lane == 0) fills[5] = nfill;
   } else if (warp == 1 || warp == 12) {
