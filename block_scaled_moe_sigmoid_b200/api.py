@@ -531,6 +531,7 @@ class LinearPlan:
         with torch.cuda.device(device):
             self.handle = moe_linear_create(T_max, N, K)
             self.workspace = torch.empty(moe_linear_workspace_bytes(self.handle), dtype=torch.uint8, device=device)
+            torch.cuda.current_stream(self.workspace.device).synchronize()   # the memory's earlier user
             moe_linear_set_workspace(self.handle, self.workspace)
 
     def forward(self, q, scale, weights, y=None, dtype=torch.bfloat16, stream=None):
@@ -581,6 +582,7 @@ class Plan:
             _call("moe_plan_set_latent", self.handle, d_latent, ctypes.c_float(eps))
         n = moe_plan_workspace_bytes(self.handle)
         self.workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+        torch.cuda.current_stream(self.workspace.device).synchronize()   # the memory's earlier user
         moe_plan_set_workspace(self.handle, self.workspace)
 
     def route(self, x, W_r, bias=None, logits=None, stream=None):

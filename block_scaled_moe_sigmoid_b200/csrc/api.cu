@@ -426,6 +426,7 @@ moe_status_t moe_plan_set_workspace(moe_plan_t p, void* dev_ptr, size_t bytes) {
   p->planes_of = nullptr;   // the router planes live in the workspace
   if (cudaMemset(p->ws + p->o_status, 0, 256) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemset(p->ws + p->o_fcnt, 0, (size_t)kFewMaxCtas * 4) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) return MOE_ERR_CUDA;
   return MOE_OK;
 }
 

@@ -178,7 +178,8 @@ moe_status_t moe_linear_set_workspace(moe_linear_t p, void* dev_ptr, size_t byte
   if (bytes < p->total) return MOE_ERR_INVALID_ARG;
   p->ws = (char*)dev_ptr;
   // the status word and the tile counters
-  if (cudaMemset(p->ws, 0, p->o_part) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaMemset(p->ws, 0, p->o_part) != cudaSuccess || cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess)
+    return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
@@ -294,8 +295,9 @@ moe_status_t moe_forward_decode(moe_plan_t p, const void* x, const uint8_t* q, c
                                 const moe_shared_bf16* sh, void* y, void* stream) {
   if (!p || T < 0 || p->dl > 0) return MOE_ERR_INVALID_ARG;   // no latent form
   if (T > p->T_max || T > kFewRows || few_stages(FEW_GLU, T, p->k, p->d / 128) < kFewMinStages ||
-      few_stages(FEW_DOWN, T, p->k, p->I / 128) < kFewMinStages)
-    return MOE_ERR_UNSUPPORTED_SHAPE;
+      few_stages(FEW_DOWN, T, p->k, p->I / 128) < kFewMinStages ||
+      (long long)p->E * (p->I / 128) * std::max(p->d / 128, (p->d + 255) / 256) * 256 > 0x7fffffffll)
+    return MOE_ERR_UNSUPPORTED_SHAPE;   // (tensor-map coordinates are 32-bit)
   if (T == 0) return MOE_OK;
   if ((q != nullptr) != (scale != nullptr) || (!x && (!q || p->Is > 0))) return MOE_ERR_INVALID_ARG;
   if (!idx || !w || !ex || !y || !ex->w_gu || !ex->s_gu || !ex->w_dn || !ex->s_dn) return MOE_ERR_INVALID_ARG;

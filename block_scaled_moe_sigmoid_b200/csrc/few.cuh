@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   // loads that the first barrier covers: the ids, or the token scales
   if constexpr (MODE != FEW_LINEAR) {
     for (int i = tid; i < slots; i += kFewThreads) {
-      s_idx[i] = a.idx[i];
+      s_idx[i] = __ldcg(a.idx + i);   // past L1: FEW_DOWN reads before its wait
       tokens[i] = 0;
     }
     for (int i = tid; i < 128; i += kFewThreads) bitmap[i] = 0;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if constexpr (MODE == FEW_DOWN) {
       // the tokens' weights, while the first steps load; an expert that a token names twice counts
       // with the sum of both, in slot order
-      for (int i = et; i < slots; i += 256) s_w[i] = a.w[i];
+      for (int i = et; i < slots; i += 256) s_w[i] = __ldcg(a.w + i);
       few_bar();
       for (int i = et; i < used * a.T; i += 256) {
         const int e = elist[i / a.T], t = i % a.T;

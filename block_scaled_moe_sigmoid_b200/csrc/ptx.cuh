@@ -234,8 +234,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 // kernel on the stream has finished.  griddep_wait() blocks until that kernel has completed
 // and its memory operations are visible; every kernel of the layer calls it before its first
 // global memory access (read or write), so only prologue work (barrier setup, TMEM
-// allocation, tensor-map prefetch) overlaps the previous kernel's tail.  Without a
-// programmatic dependency both instructions do nothing.
+// allocation, tensor-map prefetch) overlaps the previous kernel's tail.  (One exception, with
+// its reasons there: FEW_DOWN in few.cuh.)  Without a programmatic dependency both
+// instructions do nothing.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Let the next kernel on the stream begin launching (its CTAs still wait in griddep_wait).
 __device__ __forceinline__ void griddep_launch_dependents() {

@@ -26,7 +26,9 @@
  *     moe_plan_stage_ms.  The layer's kernels are launched with programmatic stream
  *     serialization: each may start its prologue while the previous kernel on the stream
  *     finishes, but touches no global memory before that kernel has completed, so stream
- *     order holds for the caller's work before and after as usual.
+ *     order holds for the caller's work before and after as usual.  (moe_forward_decode's
+ *     second kernel begins to read the ids, the routing weights and the packed weights while
+ *     its first one finishes; everything before the call is complete by then.)
  *   - Errors are returned as moe_status_t; nothing is thrown.  Argument checks happen
  *     before any launch, so an error return leaves outputs untouched.
  *   - Device-side faults (an out-of-range expert id, a pipeline wait that timed out) are
@@ -114,7 +116,8 @@ moe_status_t moe_plan_create(int T_max, int d, int E, int k, int I, int I_shared
 /* Device workspace the plan needs for T_max tokens, in bytes (host output). */
 moe_status_t moe_plan_workspace_bytes(moe_plan_t plan, size_t* bytes);
 /* Attach caller-owned device workspace (256-byte aligned, >= moe_plan_workspace_bytes).
- * The plan borrows it until destroyed or given another one. */
+ * The plan borrows it until destroyed or given another one.  Zeroes the status word and the
+ * tile counters and waits for that: earlier work on this memory has to be complete. */
 moe_status_t moe_plan_set_workspace(moe_plan_t plan, void* dev_ptr, size_t bytes);
 /* Synchronises `stream`, returns MOE_ERR_TIMEOUT / MOE_ERR_DEVICE_FAULT if a kernel since
  * the last check flagged one (bit values in *device_bits, may be NULL), and clears it. */
@@ -281,9 +284,10 @@ moe_status_t moe_add_rmsnorm_mxfp8(const void* x_bf16, const void* residual, moe
 
 /* ---- MXFP4 linear --------------------------------------------------------------------------
  * y[t] = W x[t] for a weight matrix W [N][K] in MXFP4 and rows x in MXFP8 (both with one E8M0
- * scale per 32 elements along K, accumulation in fp32).  Up to 16 rows run as
- * a stream of the weights over all SMs, more rows on the tensor cores' block-scaled GEMM; both
- * read the same packed weights.
+ * scale per 32 elements along K, accumulation in fp32).  Up to 16 rows run as one stream of the
+ * weights over all SMs, more rows as tiles of up to 176 of them, whole or split along K by
+ * whichever takes less time; all read the same packed weights.  Sums are taken in an order that
+ * depends on the shape alone.
  * moe_linear_create: a host object for calls of up to T_max rows on matrices of one shape;
  * N >= 1, K % 128 == 0, K <= 2^22, and at most 2^30 / 256 tiles of 256 x 128.  Workspace, check and destroy
  * as for moe_plan_*: caller-owned device memory, one call at a time per object. */
@@ -317,7 +321,8 @@ moe_status_t moe_linear_mxfp4(moe_linear_t linear, const uint8_t* q_e4m3, const 
  * x_bf16: device [T][d], read by the shared expert and, without q, quantised to MXFP8; it may be
  * NULL when q is given and the plan has no shared expert.  q_e4m3 / scale_e8m0: device [T][d] /
  * [T][d/32], the MXFP8 form of the tokens (moe_add_rmsnorm_mxfp8, moe_quant_mxfp8), or both NULL.
- * Other arguments as moe_forward.  An id outside [0, E) contributes nothing and is flagged
+ * Other arguments as moe_forward.  Two kernels (three when x is quantised here); the stages
+ * MOE_STAGE_GATE_UP and MOE_STAGE_DOWN hold the shared expert and the combine too.  An id outside [0, E) contributes nothing and is flagged
  * (MOE_ERR_DEVICE_FAULT at moe_plan_check); an expert that a token names twice counts with the
  * sum of both weights.  T <= 16 (and d up to 200,000); not for latent plans (MOE_ERR_INVALID_ARG).  Uses the
  * plan workspace (one call at a time per plan). */

@@ -80,6 +80,15 @@ def test_norm_in_place_and_subsets_of_outputs():
     xc = x.clone()
     got = api.moe_add_rmsnorm_mxfp8(xc, gamma, 1e-5, xn=xc)    # the norm over its own input
     assert same_bytes(xc, api.moe_add_rmsnorm_mxfp8(x, gamma, 1e-5)[1]) and got[1] is xc
+    # the same where rows stream through a resident grid
+    rows, cols = 700, 4352
+    x, gamma, res = randn((rows, cols), 6, dtype=torch.bfloat16), 1 + randn((cols,), 7, 0.1), randn((rows, cols), 8, 2.0, torch.bfloat16)
+    want = api.moe_add_rmsnorm_mxfp8(x, gamma, 1e-5, residual=res)
+    buf, xc = res.clone(), x.clone()
+    got = api.moe_add_rmsnorm_mxfp8(xc, gamma, 1e-5, residual=buf, residual_out=buf, xn=xc)
+    assert all(same_bytes(a, b) for a, b in zip(got, want))
+    only = api.moe_add_rmsnorm_mxfp8(x, gamma, 1e-5, residual=res, with_xn=False, with_mx=False)
+    assert same_bytes(only[0], want[0])
     none = api.moe_add_rmsnorm_mxfp8(x[:0], gamma)
     assert none[1].shape == (0, cols) and none[3].shape == (0, cols // 32)
 
@@ -406,6 +415,52 @@ def test_forward_decode_writes_its_rows_only():
     assert bool((buf[T * d:] == 7).all())
 
 
+def test_forward_decode_follows_a_router_that_writes_in_place():
+    """The second kernel begins before the first is done; ids and weights that the kernel before them has
+    just written, over those of the last step, are the ones it uses."""
+    T, d, E, k = 4, 256, 64, 8
+    case = Case(synth.custom(seed=21, T=T, d=d, E=E, k=k, I=128))
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, dtype=torch.float32, device="cuda")
+    xs = [randn((T, d), 300 + i, dtype=torch.bfloat16) for i in range(60)]
+    got = []
+    for x in xs:
+        api.moe_route(case.plan.handle, x, case.W_r, case.bias, k, idx=idx, w=w)
+        got.append(case.plan.forward_decode(x, idx, w, case.experts))
+    torch.cuda.synchronize()
+    for x, y in zip(xs, got):
+        i2, w2 = case.plan.route(x, case.W_r, case.bias)
+        torch.cuda.synchronize()
+        assert torch.equal(case.plan.forward_decode(x, i2, w2, case.experts), y)
+        torch.cuda.synchronize()
+    assert case.plan.check()[0] == 0
+
+
+def test_plans_made_and_used_on_another_stream():
+    """The workspace may be memory that other work of that stream was still using."""
+    T, N, K, d, E, k = 3, 2048, 2048, 512, 16, 4
+    q, s, lin, w = linear_case(T, N, K, 77)
+    case = Case(synth.custom(seed=8, T=T, d=d, E=E, k=k, I=256))
+    idx, wt = draws(T, E, k, 2)
+    want = case.plan.forward_decode(case.x, idx, wt, case.experts)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            n = 64 << 20
+            junk = torch.empty(n, dtype=torch.uint8, device="cuda")
+            for _ in range(20):
+                junk.fill_(255)
+            del junk                                   # its block goes to the next plan while the fills run
+            plan = api.LinearPlan(T, N, K)
+            y = plan.forward(q, s, lin)
+            layer_plan = api.Plan(T, d, E, k, 256)
+            z = layer_plan.forward_decode(case.x, idx, wt, case.experts)
+            assert plan.check(side)[0] == 0 and layer_plan.check(side)[0] == 0
+            check_linear(q, s, w, y)
+            assert torch.equal(z, want)
+
+
 # ---------------------------------------------------------------- the three in a row
 @pytest.mark.parametrize("T, res", [(1, torch.bfloat16), (6, torch.float32)])
 def test_a_decode_step(T, res):
@@ -433,5 +488,30 @@ def test_a_decode_step(T, res):
     ref = layer.moe_layer(xn.double().cpu().numpy(), idx.cpu().numpy(), w.cpu().numpy(), case.oracle_expert, case.oracle_shared())
     r, _ = layer.relative_errors(y.double().cpu().numpy(), ref)
     assert r.max() <= 2e-2 and r.mean() <= 2e-3
+    # the whole step captured once and replayed on another residual
+    out = {}
+
+    def step():
+        a = api.moe_add_rmsnorm_mxfp8(case.x, gamma[0], residual=resid)
+        i, v = case.plan.route(a[1], case.W_r, case.bias)
+        z = case.plan.forward_decode(a[1], i, v, case.experts, case.shared, q=a[2], scale=a[3])
+        b = api.moe_add_rmsnorm_mxfp8(z, gamma[1], residual=a[0])
+        out["logits"] = lplan.forward(b[2], b[3], lin, dtype=torch.float32)
+        return out["logits"]
+
+    assert torch.equal(step(), logits)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    captured = out["logits"]
+    keep = resid.clone()
+    resid.copy_(randn((T, d), 99, 1.0, res))
+    g.replay()
+    first = captured.clone()
+    assert torch.equal(step(), first) and not torch.equal(first, logits)
+    resid.copy_(keep)
+    g.replay()
+    assert torch.equal(captured, logits)
     check_norm(y, gamma[1], 1e-5, r1, (r2, xn2, q2, s2))
     check_linear(q2, s2, w_out, logits)
