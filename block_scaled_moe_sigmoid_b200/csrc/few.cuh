@@ -386,9 +386,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         continue;
       }
       for (int i = 0; i < r.n; ++i) {
-        int got = 1;
-        if (lane == 0) got = mbar_wait(smem_u32(sf_full + stage), phase, a.status, abort_flag);
-        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(sf_full + stage), phase, a.status, abort_flag));
         if (!ok) break;
         if constexpr (MODE != FEW_DOWN) {
           // the token scales' atom: row t's four bytes at 16 t (its last reader, the copy of the
@@ -398,10 +396,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           fence_async_shared();
           __syncwarp();
         }
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t desc = sf_desc0 + (uint64_t)((stage * kFewSF) >> 4);
-          const uint32_t tsf = tmem_base + 64 + 16 * stage;
+        tc_fence_after();
+        const uint64_t desc = sf_desc0 + (uint64_t)((stage * kFewSF) >> 4);
+        const uint32_t tsf = tmem_base + 64 + 16 * stage;
+        if (elect_one()) {
           tc_cp_32x128b_warpx4(tsf, desc);
           tc_cp_32x128b_warpx4(tsf + 4, desc + (uint64_t)(512 >> 4));
           tc_cp_32x128b_warpx4(tsf + 8, desc + (uint64_t)(1024 >> 4));
@@ -413,7 +411,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       s = r.next;
     }
-    if (lane == 0) {
+    if (elect_one()) {
       tc_commit(smem_u32(drain_sf));   // every copy lands before TMEM is released
       mbar_wait_drain(smem_u32(drain_sf), 0);
       fills[2] = nfill;

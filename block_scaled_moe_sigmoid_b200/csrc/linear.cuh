@@ -182,24 +182,27 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
     __syncwarp();
   } else if (warp == 11) {
     // ------------------------------------------------------------- scale factors -> TMEM
-    if (lane == 0) {
-      const uint64_t desc0 = smem_desc(smem_u32(sf), 16, 128, 0);
-      const bool two = C::SFB > 512 && a.n_per > 128;
-      int stage = 0, nfill = 0;
-      uint32_t phase = 0;
-      for (int s = s0; s < s1; ++s) {
-        if (!mbar_wait(smem_u32(sf_full + stage), phase, a.status, abort_flag)) break;
-        ++nfill;
-        tc_fence_after();
-        const uint64_t desc = desc0 + (uint64_t)((stage * C::SF) >> 4);
-        const uint32_t tsf = tmem_base + C::TMEM_SF + 16 * stage;
+    const uint64_t desc0 = smem_desc(smem_u32(sf), 16, 128, 0);
+    const bool two = C::SFB > 512 && a.n_per > 128;
+    int stage = 0, nfill = 0;
+    uint32_t phase = 0;
+    for (int s = s0; s < s1; ++s) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(sf_full + stage), phase, a.status, abort_flag))) break;
+      ++nfill;
+      tc_fence_after();
+      const uint64_t desc = desc0 + (uint64_t)((stage * C::SF) >> 4);
+      const uint32_t tsf = tmem_base + C::TMEM_SF + 16 * stage;
+      if (elect_one()) {
         tc_cp_32x128b_warpx4(tsf, desc);
         tc_cp_32x128b_warpx4(tsf + 4, desc + (uint64_t)(512 >> 4));
         tc_cp_32x128b_warpx4(tsf + 8, desc + (uint64_t)(1024 >> 4));
         if (two) tc_cp_32x128b_warpx4(tsf + 12, desc + (uint64_t)(1536 >> 4));
         tc_commit(smem_u32(full_bar + stage));
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
+      __syncwarp();
+      if (++stage == STAGES) { stage = 0; phase ^= 1; }
+    }
+    if (elect_one()) {
       tc_commit(smem_u32(drain_sf));   // every copy lands before TMEM is released
       mbar_wait_drain(smem_u32(drain_sf), 0);
       fills[2] = nfill;
