@@ -2,8 +2,8 @@
 //
 //   FEW_LINEAR  y[t] = W x[t]                                    one matrix, x in MXFP8
 //   FEW_GLU     h[t,e] = MX(glu(Wg x[t], Wu x[t]))               the experts e = idx[t][j]
-//               hs[t] = bf16(glu(Vg x[t], Vu x[t]))              the shared expert, bf16
-//   FEW_DOWN    y[t] = bf16(Vd hs[t] + sum_j w[t][j] Wd h[t,j])  the same experts
+//               v[t] = bf16(glu(Vg x[t], Vu x[t]))               the shared expert, bf16
+//   FEW_DOWN    y[t] = bf16(Vd v[t] + sum_j w[t][j] Wd h[t,j])   the same experts
 //
 // With so few rows every weight byte is used once and the bytes are the cost: 17/32 byte per
 // weight at the copy rate of the memory.  The work is one list of steps, a step being one 256-row
@@ -33,6 +33,14 @@
 // box per step), warp 11 moves each step's scales into TMEM, warps 1 and 12 issue the MMAs of one
 // 128-row half each (one thread forms and issues an instruction in about 90 cycles, and eight of them
 // would take longer than the step's load), warps 2 to 9 run the epilogue, a thread per weight row.
+// The scale and MMA warps run converged and elect the lane that issues: formed in a branch of one lane,
+// each operand goes to its uniform register by itself, and the scale warp alone then held the stream at
+// 5.9 TB/s.
+//
+// Measured (B200, copy rate 6.54 TB/s): 8 tokens on 58 experts of 3584 x 3072 in 153 us, 6.6 TB/s; one
+// token on 16 experts of 7168 x 3072 in 93.4 us, 6.0 TB/s (113 us with a shared expert); 8 rows of
+// 40000 x 7168 in 27.0 us, 5.6 TB/s.  Around the stream each kernel takes about 4 us for its tables, the
+// first load's latency and the last exchange; small shapes are that latency.
 #pragma once
 #include <type_traits>
 
@@ -72,7 +80,7 @@ struct FewArgs {
   uint8_t* hs;            // scale atoms of h, [used expert][k-tile][512]
   void* y;
   int y_f32;
-  float* part;            // [2 per CTA][T][256]
+  float* part;            // [2 per CTA][16][256]
   unsigned int* counters; // [CTAs], zero between launches
   unsigned int* status;
 };
@@ -108,7 +116,7 @@ __device__ __forceinline__ unsigned int count_acq_rel(unsigned int* counter) {
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Steps that stay together in a CTA: a whole tile, or one step.  Split tiles cost the exchange of
 // partials, about 3 us at the end of the call, the time of kFewSplitCost steps; whole tiles cost the
-// last wave's idle CTAs.
+// last wave's idle CTAs (5 rows of 1003 x 640, four tiles of five steps: 5.8 us whole, 8.0 split).
 constexpr int kFewSplitCost = 8;
 __host__ __device__ inline int few_unit(int tiles, int KT, int grid) {
   const long long total = (long long)tiles * KT;
@@ -419,8 +427,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __syncwarp();
   } else if (warp == 1 || warp == 12) {
     // ------------------------------------------------------------- MMA issuers, one per 128-row half
-    // The warp runs the loop together and elects the lane that issues: in a branch of one lane the
-    // operands of every MMA would be moved to uniform registers one by one.
     const int h = warp == 12;
     const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, 2);
     int stage = 0, nfill = 0, nrun = 0;
