@@ -38,7 +38,7 @@
 // 5.9 TB/s.
 //
 // Measured (B200, copy rate 6.54 TB/s): 8 tokens on 58 experts of 3584 x 3072 in 153 us, 6.6 TB/s; one
-// token on 16 experts of 7168 x 3072 in 93.4 us, 6.0 TB/s (113 us with a shared expert); 8 rows of
+// token on 16 experts of 7168 x 3072 in 92.0 us, 6.1 TB/s (112 us with a shared expert); 8 rows of
 // 40000 x 7168 in 27.0 us, 5.6 TB/s.  Around the stream each kernel takes about 4 us for its tables, the
 // first load's latency and the last exchange; small shapes are that latency.
 #pragma once
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int unit = SS ? 1 : few_unit(MODE == FEW_GLU ? used * a.m_tiles : a.m_tiles, KT, gridDim.x);   // that stay together
   const long long units = total / max(unit, 1);
   // at least four steps for a CTA where tiles are split
-  const long long G = min(unit == KT ? units : max(units / 4, min(units, 1ll)), (long long)gridDim.x);
+  const long long G = min(unit == KT && !SS ? units : max(units / 4, min(units, 1ll)), (long long)gridDim.x);
   const int c = blockIdx.x;
   const int s0 = c < G ? (int)(c * units / G) * unit : 0, s1 = c < G ? (int)((c + 1) * units / G) * unit : 0;
   // A run: consecutive steps of one matrix and one tile, accumulated in TMEM: K tiles [kb, kb + n).
