@@ -274,6 +274,8 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
   a.unit = pick.unit;
   const int units = n_tiles * m_tiles * k_tiles / a.unit;
   a.ctas = std::min(a.unit == k_tiles ? units : std::max(units / 4, 1), p->grid());
+  a.per = units / a.ctas;
+  a.rem = units - a.per * a.ctas;
   a.sf = (const uint8_t*)W->s;
   a.xs = scale;
   a.y = y;

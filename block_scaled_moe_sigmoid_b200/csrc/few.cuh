@@ -118,9 +118,8 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 // partials, about 3 us at the end of the call, the time of kFewSplitCost steps; whole tiles cost the
 // last wave's idle CTAs (5 rows of 1003 x 640, four tiles of five steps: 5.8 us whole, 8.0 split).
 constexpr int kFewSplitCost = 8;
-__host__ __device__ inline int few_unit(int tiles, int KT, int grid) {
-  const long long total = (long long)tiles * KT;
-  return (long long)((tiles + grid - 1) / grid) * KT <= (total + grid - 1) / grid + kFewSplitCost ? KT : 1;
+__device__ __forceinline__ int few_unit(int tiles, int KT, int grid) {
+  return (tiles + grid - 1) / grid * KT <= (tiles * KT + grid - 1) / grid + kFewSplitCost ? KT : 1;
 }
 __device__ __forceinline__ bool elect_one() {   // one lane of the converged warp, the same one each time
   uint32_t p;
@@ -250,11 +249,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int routed = MODE == FEW_GLU ? used * a.m_tiles * RT : a.m_tiles * KT;
   const int total = routed + (MODE == FEW_GLU ? a.sh_tiles * SS : 0);
   const int unit = SS ? 1 : few_unit(MODE == FEW_GLU ? used * a.m_tiles : a.m_tiles, KT, gridDim.x);   // that stay together
-  const long long units = total / max(unit, 1);
-  // at least four steps for a CTA where tiles are split
-  const long long G = min(unit == KT && !SS ? units : max(units / 4, min(units, 1ll)), (long long)gridDim.x);
-  const int c = blockIdx.x;
-  const int s0 = c < G ? (int)(c * units / G) * unit : 0, s1 = c < G ? (int)((c + 1) * units / G) * unit : 0;
+  const int units = total / max(unit, 1);
+  // at least four steps for a CTA where tiles are split; the first `rem` CTAs take one unit more.  (All in
+  // 32 bits: the producers cannot start before this, and each 64-bit division takes a tenth of a us.)
+  const int G = min(unit == KT && !SS ? units : max(units / 4, min(units, 1)), (int)gridDim.x);
+  const int c = blockIdx.x, per = units / max(G, 1), rem = units - per * G;
+  const int s0 = c < G ? (c * per + min(c, rem)) * unit : 0, s1 = c < G ? s0 + (per + (c < rem)) * unit : 0;
+  // the CTA with step s (unit = 1)
+  auto cta_of = [&](int s) { return s < rem * (per + 1) ? s / (per + 1) : rem + (s - rem * (per + 1)) / per; };
   // A run: consecutive steps of one matrix and one tile, accumulated in TMEM: K tiles [kb, kb + n).
   // The tile is [t0, t0 + len) in the list, and its last step begins at t0 + last.
   struct Run { int tile, u, m, kb, n, next, t0, len, last; bool shared; };
@@ -551,8 +553,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int t = 0; t < kFewRows; ++t)
           if (t < a.T) mine[t * 256] = acc[t];
         few_bar();
-        // (unit = 1) the CTAs with the tile's first and last step
-        const int c_lo = (int)(((t0 + 1ll) * G - 1) / total), c_hi = (int)(((t0 + first.last + 1ll) * G - 1) / total);
+        // the CTAs with the tile's first and last step
+        const int c_lo = cta_of(t0), c_hi = cta_of(t0 + first.last);
         if (et == 0) {
           // the CTA's partial ordered before the count, the others' partials after it
           const bool last = count_acq_rel(a.counters + c_lo) == (unsigned)(c_hi - c_lo);

@@ -19,6 +19,7 @@ struct LinearArgs {
   int m_tiles, k_tiles;
   int N;
   int unit, ctas;           // steps that stay together (a whole tile, or 1), CTAs that share the units
+  int per, rem;             // units per CTA; the first `rem` CTAs take one more
   const uint8_t* sf;        // weight scales [m-tile][k-tile][1 KB]
   const uint8_t* xs;        // token scales [T][4 k_tiles]
   void* y;
@@ -27,12 +28,10 @@ struct LinearArgs {
   unsigned int* status;
 };
 // First step of CTA c's part of the list, and the CTA with step s where a unit is one step.
-__host__ __device__ inline int linear_first_step(const LinearArgs& a, int c) {
-  const long long units = (long long)a.n_tiles * a.m_tiles * a.k_tiles / a.unit;
-  return (int)(c * units / a.ctas) * a.unit;
-}
-__device__ __forceinline__ int linear_cta_of(const LinearArgs& a, long long s) {
-  return (int)(((s + 1) * a.ctas - 1) / ((long long)a.n_tiles * a.m_tiles * a.k_tiles));
+__device__ __forceinline__ int linear_first_step(const LinearArgs& a, int c) { return (c * a.per + min(c, a.rem)) * a.unit; }
+__device__ __forceinline__ int linear_cta_of(const LinearArgs& a, int s) {
+  const int big = a.rem * (a.per + 1);
+  return s < big ? s / (a.per + 1) : a.rem + (s - big) / a.per;
 }
 
 constexpr int kLinearThreads = kFewThreads + 32;   // few.cuh's roles, and warp 13
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const __grid_constant__
   griddep_wait();
   griddep_launch_dependents();
   const int tile = blockIdx.x, n = 4 * blockIdx.y, row = threadIdx.x;
-  const long long t0 = (long long)tile * a.k_tiles;
+  const int t0 = tile * a.k_tiles;
   const int lo = linear_cta_of(a, t0), hi = linear_cta_of(a, t0 + a.k_tiles - 1);
   const int m = tile / a.n_tiles, nt = tile - m * a.n_tiles;
   if (lo == hi || nt * a.n_per + n >= a.T) return;   // one CTA had the whole tile and stored it
