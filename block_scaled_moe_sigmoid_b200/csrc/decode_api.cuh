@@ -28,6 +28,10 @@ cudaError_t launch_few(FewArgs a, const CUtensorMap& tW, const CUtensorMap& tX, 
   if (e != cudaSuccess) return e;
   a.stages = few_stages(MODE, a.T, a.k, a.k_tiles);
   if (a.stages < kFewMinStages) return cudaErrorInvalidValue;   // the callers check before any launch
+  a.by_m = fast_div(a.m_tiles);
+  a.by_k = fast_div(a.k_tiles);
+  a.by_ss = fast_div(std::max(2 * a.sh_steps, 1));
+  a.by_grid = fast_div(grid);
   return launch_k(kern, grid, kFewThreads, few_smem(MODE, a.T, a.k, a.k_tiles, a.stages).total, s, a, tW, tX, tSW, tSX);
 }
 
