@@ -48,10 +48,12 @@ cudaError_t launch_linear(const LinearArgs& a, const CUtensorMap& tW, const CUte
 }
 
 // The norm's variants.  A thread holds V vectors of 8 elements: one where a row fits 1024 threads so,
-// else 2 or 4.  The streaming kernel pays where a CTA per row is so wide that only two fit an SM, and
-// there are rows enough for more than one turn: 8192 x 7168 85 us against 106, 400 x 7168 7.9 against
-// 8.6; but 8192 x 4096 59 against 51 (a CTA of 512 threads has three others beside it).
-constexpr int kNormStreamVecs = 512;
+// else 2 or 4.  The streaming kernel pays where there are rows for more than one turn and a CTA per row
+// has too few loads in flight.  With a bf16 residual that is where only two such CTAs fit an SM: 8192 x
+// 7168 85.6 us against 96.4, 400 x 7168 7.72 against 7.77; but 8192 x 4096 52.2 against 49.6.  Without
+// one, at half the loads, also narrower: 8192 x 7168 57.5 against 80.7, 8192 x 4096 32.2 against 39.3,
+// 8192 x 2048 (left as it is) 18.9 against 19.4.
+constexpr int kNormStreamVecs = 512, kNormStreamVecsPlain = 256;
 template <int RES, int V>
 cudaError_t launch_norm_rows(const NormArgs& a, cudaStream_t s) {
   const int nvec = a.cols / 8, team = ((nvec + V - 1) / V + 31) / 32 * 32, per_cta = std::max(1, 128 / team);
@@ -64,8 +66,8 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return cudaErrorInvalidDevice;
-    const int team = ((nvec + 1) / 2 + 31) / 32 * 32, grid = sms * (team > 512 ? 1 : 2);
-    if (nvec > kNormStreamVecs && nvec <= 2048 && a.rows > grid) {
+    const int team = ((nvec + 1) / 2 + 31) / 32 * 32, grid = sms * std::max(1, 1152 / team);   // as many as fit (56 registers a thread)
+    if (nvec > (RES == NORM_RES_BF16 ? kNormStreamVecs : kNormStreamVecsPlain) && nvec <= 2048 && a.rows > grid) {
       auto kern = add_rmsnorm_mxfp8_stream_kernel<RES, 2>;
       static std::atomic<uint64_t> done{0};
       const cudaError_t e = ensure_smem_attr(kern, kNormDepth * 2 * 32 * 1024, done);

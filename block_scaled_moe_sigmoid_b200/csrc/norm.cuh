@@ -151,10 +151,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormArgs 
   if (wpr > 1) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.y * wpr + (threadIdx.x >> 5)] = ss;
     __syncthreads();
-    ss = 0.0f;
-    for (int i = 0; i < wpr; ++i) ss += part[threadIdx.y * wpr + i];
+    const int lane = threadIdx.x & 31;
+    ss = norm_warp_sum(lane < wpr ? part[threadIdx.y * wpr + lane] : 0.0f);
   }
-  const float inv = rsqrtf(ss / (float)a.cols + a.eps);
+  const float inv = __frsqrt_rn(ss / (float)a.cols + a.eps);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = threadIdx.x + i * team;
@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormArgs 
 
 // Many wide rows: a resident grid walks the rows, a CTA each, and every thread keeps the loads of its
 // next three rows in flight (cp.async into shared memory that only it reads, so nothing waits but the row's sum).
-// 8192 x 7168 with a bf16 residual: 85 us, 6.2 TB/s, where a CTA per row takes 106 us (its loads stop
-// while it reduces and stores).  With an fp32 residual a CTA per row has enough loads in flight (125 us,
-// 6.1 TB/s) and the ring would hold too few rows (134 us).
+// 8192 x 7168 with a bf16 residual: 85.6 us, 6.2 TB/s, where a CTA per row takes 96 us (its loads stop
+// while it reduces and stores).  With an fp32 residual a CTA per row has enough loads in flight (117 us,
+// 6.5 TB/s) and the ring would hold too few rows (134 us).
 constexpr int kNormDepth = 3;
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -221,9 +221,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_stream_kernel(const No
     ss = norm_warp_sum(ss);
     if ((tid & 31) == 0) part[turn][tid >> 5] = ss;
     __syncthreads();   // the next turn writes the other half: one barrier a row is enough
-    ss = 0.0f;
-    for (int i = 0; i < team >> 5; ++i) ss += part[turn][i];
-    const float inv = rsqrtf(ss / (float)a.cols + a.eps);
+    ss = norm_warp_sum((tid & 31) < team >> 5 ? part[turn][tid & 31] : 0.0f);
+    const float inv = __frsqrt_rn(ss / (float)a.cols + a.eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * team;

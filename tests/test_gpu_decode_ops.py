@@ -50,7 +50,7 @@ def check_norm(x, gamma, eps, res, out):
 @pytest.mark.parametrize("res", [None, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows, cols", [(1, 32), (3, 64), (129, 96), (5, 736), (700, 1024), (1, 7168), (33, 7168), (7, 8224),
                                         (3, 16416), (2, 32768),
-                                        (301, 4128), (310, 16384), (300, 16416), (320, 30016), (1000, 7168)])
+                                        (301, 4128), (310, 16384), (300, 16416), (320, 30016), (1000, 7168), (1200, 2112), (700, 4096), (500, 6144)])
 def test_norm(rows, cols, res):
     seed = rows * 100003 + cols
     x, gamma = randn((rows, cols), seed, dtype=torch.bfloat16), 1 + randn((cols,), seed + 1, 0.1)
