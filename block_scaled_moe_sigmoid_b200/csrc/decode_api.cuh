@@ -100,7 +100,7 @@ constexpr int kLinearSmall = 64, kLinearWide = 176, kLinearMany = 1024;
 //   a step of n rows takes 255 + 0.77 n (n <= 64) or 190 + 2.1 n: up to 64 rows the issue and the weights,
 //   above them the shared memory's fill rate;
 //   exchanging partials takes 2500 + 55 n, and whole tiles the last wave's idle SMs.
-// 300 rows of 7168 x 7168: five whole tiles of 64 rows by 28 take 20.9 us, two of 160 split 27.3; 64 rows:
+// 300 rows of 7168 x 7168: five whole tiles of 64 rows by 28 take 20.1 us, two of 160 split 27.3; 64 rows:
 // one tile split 13.2, two whole ones 19.5.  Past 1024 rows wide whole tiles win for their fewer loads
 // (2048 rows: 176 100 us, 112 115, 64 139).
 struct LinearPick { int n_per, unit; };
