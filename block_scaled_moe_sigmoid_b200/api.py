@@ -490,8 +490,9 @@ class Experts:
                             self.s_dn.data_ptr())
 
     def pack(self, e, w_gate, w_up, w_down, stream=None):
-        moe_pack_expert_mxfp4(self.d, self.I, e, w_gate.contiguous(), w_up.contiguous(),
-                              w_down.contiguous(), self, stream)
+        with _On(self.w_gu.get_device(), stream):   # copies of strided weights belong to the stream that packs them
+            moe_pack_expert_mxfp4(self.d, self.I, e, w_gate.contiguous(), w_up.contiguous(),
+                                  w_down.contiguous(), self)
 
 
 class Shared:
@@ -504,8 +505,9 @@ class Shared:
         return SharedBF16(self.w_gu.data_ptr(), self.w_dn.data_ptr())
 
     def pack(self, w_gate, w_up, w_down, stream=None):
-        moe_pack_shared_bf16(self.d, self.I_shared, w_gate.contiguous(), w_up.contiguous(),
-                             w_down.contiguous(), self, stream)
+        with _On(self.w_gu.get_device(), stream):   # as Experts.pack
+            moe_pack_shared_bf16(self.d, self.I_shared, w_gate.contiguous(), w_up.contiguous(),
+                                 w_down.contiguous(), self)
 
 
 class LinearMXFP4:
@@ -519,7 +521,8 @@ class LinearMXFP4:
         return MatrixMXFP4(self.w.data_ptr(), self.s.data_ptr())
 
     def pack(self, w, stream=None):
-        moe_pack_linear_mxfp4(self.N, self.K, w.contiguous(), self, stream)
+        with _On(self.w.get_device(), stream):   # as Experts.pack
+            moe_pack_linear_mxfp4(self.N, self.K, w.contiguous(), self)
 
 
 class LinearPlan:

@@ -141,3 +141,38 @@ def test_binding_refuses_what_a_pointer_cannot_carry():
             api._checked("t", t, dtype, shape, host)
     with pytest.raises(ValueError):
         api._checked("t", ok, torch.float32, (4, 8), 0)
+
+
+def test_packing_copies_strided_weights_on_its_own_stream(monkeypatch):
+    """The copy that makes a strided weight contiguous is ordered with the packing that reads it, and its memory goes
+    back to that stream."""
+    packed = [api.LinearMXFP4(64, 128, device="cpu"), api.Experts(128, 128, 1, device="cpu"), api.Shared(128, 128, device="cpu")]
+    log = []
+
+    class On:
+        def __init__(self, index, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            log.append(("on", self.stream))
+
+        def __exit__(self, *exc):
+            log.append("off")
+
+    class Weight(torch.Tensor):
+        def contiguous(self):
+            log.append("copy")
+            return torch.Tensor.contiguous(self).as_subclass(torch.Tensor)
+
+    monkeypatch.setattr(api, "_On", On)
+    monkeypatch.setattr(api, "_elsewhere", lambda index, stream: stream is not None)
+    monkeypatch.setattr(api, "_stream", lambda stream=None: stream)
+    monkeypatch.setattr(api, "_raw_stream", lambda index: None)
+    monkeypatch.setattr(api, "_call", lambda name, *args: log.append(name))
+    square, tall = torch.zeros(128, 128).as_subclass(Weight).t(), torch.zeros(128, 64).as_subclass(Weight).t()
+    for buffers, args in zip(packed, ((tall,), (0, square, square, square), (square, square, square))):
+        log.clear()
+        buffers.pack(*args, stream="side")
+        copies = sum(isinstance(a, torch.Tensor) for a in args)
+        assert log[0] == ("on", "side") and log[-1] == "off" and log[1:-2] == ["copy"] * copies
+        assert log[-2].startswith("moe_pack_")

@@ -263,6 +263,33 @@ def test_linear_two_plans_on_two_streams_and_graph_replay():
     assert all(p.check()[0] == 0 for p in plans)
 
 
+def test_packing_a_strided_weight_on_a_side_stream():
+    """Packed while the current stream is busy, and its pool's memory in use: the bytes are those of the contiguous weight."""
+    N = K = 512
+    w = randn((K, N), 5, 0.02)
+    sw = randn((K, N), 6, 0.02, torch.bfloat16)
+    want, got = [(api.LinearMXFP4(N, K), api.Experts(K, N, 1), api.Shared(K, N)) for _ in range(2)]
+
+    def pack(buffers, m, b, stream=None):
+        buffers[0].pack(m, stream=stream)
+        buffers[1].pack(0, m, m, m, stream=stream)
+        buffers[2].pack(b, b, b, stream=stream)
+
+    pack(want, w.t().contiguous(), sw.t().contiguous())
+    side, junk = torch.cuda.Stream(), torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        junk.fill_(255)
+    pack(got, w.t(), sw.t(), side)
+    for _ in range(4):                      # what the current stream allocates next is not what the packing reads
+        torch.empty(N * K, dtype=torch.float32, device="cuda").fill_(7.0)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for name in ("w", "s", "w_gu", "s_gu", "w_dn", "s_dn"):
+            if hasattr(a, name):
+                assert same_bytes(getattr(a, name), getattr(b, name)), (type(a).__name__, name)
+
+
 # ---------------------------------------------------------------- the layer for a few tokens
 def check_decode(case, idx, w, y, T=None):
     rows = case.x_np() if T is None else case.x_np()[:T]
