@@ -368,6 +368,23 @@ static cudaError_t run_permute(moe_plan_s* p, const int32_t* idx, int T, int bn,
   return cudaGetLastError();
 }
 
+// The device bits that calls on `s` have flagged, read and cleared.  The resets run on `s` and have
+// finished on return: a stream that does not order itself after the legacy one would let the next call
+// start beside them, and lose its count of a tile's partials or its own flag.  Only a kernel that gave up
+// can leave a tile counter behind.
+static moe_status_t take_status(unsigned int* status, unsigned int* counters, cudaStream_t s, unsigned int* bits) {
+  unsigned int v = 0;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaMemcpy(&v, status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
+  if (v && cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((v & MOE_DEV_ERR_TIMEOUT) && cudaMemsetAsync(counters, 0, (size_t)kFewMaxCtas * 4, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (v && cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (bits) *bits = v;
+  if (v & MOE_DEV_ERR_TIMEOUT) return MOE_ERR_TIMEOUT;
+  if (v) return MOE_ERR_DEVICE_FAULT;
+  return MOE_OK;
+}
+
 extern "C" {
 
 const char* moe_status_string(moe_status_t s) {
@@ -433,16 +450,7 @@ moe_status_t moe_plan_set_workspace(moe_plan_t p, void* dev_ptr, size_t bytes) {
 moe_status_t moe_plan_check(moe_plan_t p, void* stream, unsigned int* bits) {
   if (!p) return MOE_ERR_INVALID_ARG;
   if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
-  unsigned int v = 0;
-  if (cudaStreamSynchronize(S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaMemcpy(&v, p->ws + p->o_status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaMemset(p->ws + p->o_status, 0, 4) != cudaSuccess) return MOE_ERR_CUDA;
-  // a kernel that gave up may have left a tile counter behind
-  if (v && cudaMemset(p->ws + p->o_fcnt, 0, (size_t)kFewMaxCtas * 4) != cudaSuccess) return MOE_ERR_CUDA;
-  if (bits) *bits = v;
-  if (v & MOE_DEV_ERR_TIMEOUT) return MOE_ERR_TIMEOUT;
-  if (v) return MOE_ERR_DEVICE_FAULT;
-  return MOE_OK;
+  return take_status(p->at<unsigned int>(p->o_status), p->at<unsigned int>(p->o_fcnt), S(stream), bits);
 }
 
 moe_status_t moe_plan_destroy(moe_plan_t p) {

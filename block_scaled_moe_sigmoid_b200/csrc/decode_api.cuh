@@ -192,15 +192,7 @@ moe_status_t moe_linear_set_workspace(moe_linear_t p, void* dev_ptr, size_t byte
 moe_status_t moe_linear_check(moe_linear_t p, void* stream, unsigned int* bits) {
   if (!p) return MOE_ERR_INVALID_ARG;
   if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
-  unsigned int v = 0;
-  if (cudaStreamSynchronize(S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaMemcpy(&v, p->ws + p->o_status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  // a kernel that gave up may have left a tile counter behind
-  if (v && cudaMemset(p->ws, 0, p->o_part) != cudaSuccess) return MOE_ERR_CUDA;
-  if (bits) *bits = v;
-  if (v & MOE_DEV_ERR_TIMEOUT) return MOE_ERR_TIMEOUT;
-  if (v) return MOE_ERR_DEVICE_FAULT;
-  return MOE_OK;
+  return take_status(p->at<unsigned int>(p->o_status), p->at<unsigned int>(p->o_cnt), S(stream), bits);
 }
 
 moe_status_t moe_linear_destroy(moe_linear_t p) {

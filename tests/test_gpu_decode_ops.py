@@ -373,6 +373,31 @@ def test_forward_decode_ids_outside_and_named_twice():
     assert case.plan.check()[0] == 0
 
 
+def test_check_is_done_with_the_workspace_when_it_returns():
+    """On a stream that does not order itself after the legacy one, calls right after a check that has flags to clear:
+    the check leaves the tile counters and the status word alone from then on."""
+    T, E, k = 4, 16, 4
+    case = Case(synth.custom(seed=31, T=T, d=1024, E=E, k=k, I=512, I_shared=512))
+    idx, w = draws(T, E, k, 6)
+    bad = torch.full_like(idx, E)
+    want = case.plan.forward_decode(case.x, idx, w, case.experts, case.shared)
+    assert case.plan.check()[0] == 0
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for i in range(100):
+        case.plan.forward_decode(case.x, bad, w, case.experts, case.shared, stream=side)
+        assert case.plan.check(side) == (7, 2)               # MOE_ERR_DEVICE_FAULT, the bounds bit
+        got.append(case.plan.forward_decode(case.x, idx, w, case.experts, case.shared, stream=side))
+        if i % 10 == 0:
+            assert case.plan.check(side) == (0, 0)
+            api.moe_debug_timeout_probe(case.plan.handle, side) if i == 50 else None
+            assert case.plan.check(side)[0] == (5 if i == 50 else 0)
+            got.append(case.plan.forward_decode(case.x, idx, w, case.experts, case.shared, stream=side))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got) and case.plan.check(side) == (0, 0)
+
+
 def test_forward_decode_tokens_that_are_not_finite_keep_to_themselves():
     T, E, k = 4, 8, 2
     case = Case(synth.custom(seed=4, T=T, d=256, E=E, k=k, I=128))
