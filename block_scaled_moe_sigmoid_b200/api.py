@@ -52,6 +52,7 @@ SIGNATURES = {
     "moe_linear_set_workspace": [_P, _P, _S],
     "moe_linear_check": [_P, _P, ctypes.POINTER(ctypes.c_uint)],
     "moe_linear_destroy": [_P],
+    "moe_linear_tiling": [_P, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)],
     "moe_linear_bytes": [_I, _I, ctypes.POINTER(_S), ctypes.POINTER(_S)],
     "moe_pack_linear_mxfp4": [_I, _I, _P, _P, _P],
     "moe_linear_mxfp4": [_P, _P, _P, _I, _P, _P, _I, _P],
@@ -386,6 +387,13 @@ def moe_linear_check(linear, stream=None):
 
 def moe_linear_destroy(linear):
     _call("moe_linear_destroy", linear)
+
+
+def moe_linear_tiling(linear, T):
+    """(token rows of a tile, or 0 where a call with T rows is a stream of the weights; whether tiles are split along K)."""
+    rows, split = ctypes.c_int(), ctypes.c_int()
+    _call("moe_linear_tiling", linear, T, ctypes.byref(rows), ctypes.byref(split))
+    return rows.value, bool(split.value)
 
 
 def moe_linear_bytes(N, K):

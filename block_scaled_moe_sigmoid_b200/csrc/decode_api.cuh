@@ -93,33 +93,38 @@ struct moe_linear_s {
 };
 // linear_kernel's tiles: up to 64 token rows with five pipeline stages, or up to 176 (the widest whose
 // accumulators, with four stages' scales, fit the tensor memory and whose stages fit shared memory).
-constexpr int kLinearSmall = 64, kLinearWide = 176, kLinearMany = 1024;
+constexpr int kLinearSmall = 64, kLinearWide = 176;
 
 // Token rows per tile (a multiple of 16) and whether tiles stay whole, by the time each choice takes, in
-// ns, fitted to 7168 x 7168, 7168 x 1024, 1003 x 7168 and 40000 x 7168 with 32 to 1024 rows:
+// ns, for every number of rows:
 //   a step of n rows takes 255 + 0.77 n (n <= 64) or 190 + 2.1 n: up to 64 rows the issue and the weights,
 //   above them the shared memory's fill rate;
-//   exchanging partials takes 2500 + 55 n, and whole tiles the last wave's idle SMs.
-// 300 rows of 7168 x 7168: five whole tiles of 64 rows by 28 take 20.1 us, two of 160 split 27.3; 64 rows:
-// one tile split 13.2, two whole ones 19.5.  Past 1024 rows wide whole tiles win for their fewer loads
-// (2048 rows: 176 100 us, 112 115, 64 139).
+//   whole tiles cost the last wave's idle SMs;
+//   exchanging partials takes 2500 + 55 n, and 0.8 for each CTA of the kernel that adds them, four token
+//   rows of a tile each (without it 2700 rows of 7168 x 7168 are split, 159 us instead of 122 whole, and
+//   1024 rows of 28672 x 7168, 233 instead of 197).
+// Fitted to ten shapes from 256 x 7168 to 28672 x 7168 with 17 to 8192 rows, every height and both forms
+// timed: the choice takes 1.1% more than the best one on average.  300 rows of 7168 x 7168: five whole
+// tiles of 64 rows by 28 take 20.9 us, 64 rows: one tile split 13.4, two whole ones 19.5.
 struct LinearPick { int n_per, unit; };
 LinearPick pick_linear_tiles(int T, int m_tiles, int k_tiles, int grid) {
-  if (T > kLinearMany) return {kLinearWide, k_tiles};
   LinearPick best = {kLinearWide, k_tiles};
   double best_ns = 1e30;
   for (int n = 16; n <= kLinearWide; n += 16) {
     const long long tiles = (long long)((T + n - 1) / n) * m_tiles, steps = tiles * k_tiles;
+    if (steps > 0x7fffffffll) continue;   // the kernel counts steps in 32 bits
     const double step = n <= kLinearSmall ? 255.0 + 0.77 * n : 190.0 + 2.1 * n;
     const double whole = (double)((tiles + grid - 1) / grid) * k_tiles * step;
     const long long ctas = std::max(std::min(steps / 4, (long long)grid), 1ll);
-    const double split = (double)((steps + ctas - 1) / ctas) * step + 2500.0 + 55.0 * n;
+    const double split = (double)((steps + ctas - 1) / ctas) * step + 2500.0 + 55.0 * n + 0.8 * (double)(tiles * (n / 4));
     if (whole < best_ns) { best_ns = whole; best = {n, k_tiles}; }
     if (k_tiles > 1 && split < best_ns) { best_ns = split; best = {n, 1}; }
     if (n >= T) break;
   }
   return best;
 }
+// Whether a call with T rows is a stream of the weights (few.cuh).
+bool linear_streams(int T, int k_tiles) { return T <= kFewRows && few_stages(FEW_LINEAR, T, 0, k_tiles) >= kFewMinStages; }
 
 extern "C" {
 
@@ -195,6 +200,18 @@ moe_status_t moe_linear_check(moe_linear_t p, void* stream, unsigned int* bits) 
   return take_status(p->at<unsigned int>(p->o_status), p->at<unsigned int>(p->o_cnt), S(stream), bits);
 }
 
+moe_status_t moe_linear_tiling(moe_linear_t p, int T, int* rows, int* split) {
+  if (!p || T < 0 || !rows || !split) return MOE_ERR_INVALID_ARG;
+  if (T > p->T_max) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const int k_tiles = p->K / 128;
+  *rows = *split = 0;
+  if (T == 0 || linear_streams(T, k_tiles)) return MOE_OK;
+  const LinearPick pick = pick_linear_tiles(T, (p->N + 255) / 256, k_tiles, p->grid());
+  *rows = pick.n_per;
+  *split = pick.unit < k_tiles;
+  return MOE_OK;
+}
+
 moe_status_t moe_linear_destroy(moe_linear_t p) {
   if (!p) return MOE_ERR_INVALID_ARG;
   delete p;
@@ -237,7 +254,7 @@ moe_status_t moe_linear_mxfp4(moe_linear_t p, const uint8_t* q, const uint8_t* s
   if (!p->ws) return MOE_ERR_NOT_INITIALIZED;
   cudaStream_t s = S(stream);
   const int N = p->N, K = p->K, k_tiles = K / 128, m_tiles = (N + 255) / 256;
-  if (T <= kFewRows && few_stages(FEW_LINEAR, T, 0, k_tiles) >= kFewMinStages) {
+  if (linear_streams(T, k_tiles)) {
     CUtensorMap tW, tX;
     if (!make_few_maps(&tW, &tX, W->w, (uint64_t)m_tiles * k_tiles, q, T, K)) return MOE_ERR_CUDA;
     FewArgs a;

@@ -304,6 +304,9 @@ moe_status_t moe_linear_workspace_bytes(moe_linear_t linear, size_t* bytes);
 moe_status_t moe_linear_set_workspace(moe_linear_t linear, void* dev_ptr, size_t bytes);
 moe_status_t moe_linear_check(moe_linear_t linear, void* stream, unsigned int* device_bits);
 moe_status_t moe_linear_destroy(moe_linear_t linear);
+/* How a call with T rows is cut (host outputs, no GPU work): the token rows of a tile, 0 where the call
+ * is a stream of the weights, and whether tiles are split along K. */
+moe_status_t moe_linear_tiling(moe_linear_t linear, int T, int* rows_per_tile, int* split);
 /* Byte sizes of a packed matrix (host outputs). */
 moe_status_t moe_linear_bytes(int N, int K, size_t* w, size_t* s);
 /* MXFP4-quantise fp32 W (device [N][K], 16-byte aligned) into `dst`, as moe_pack_expert_mxfp4. */

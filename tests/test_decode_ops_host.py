@@ -176,3 +176,40 @@ def test_packing_copies_strided_weights_on_its_own_stream(monkeypatch):
         copies = sum(isinstance(a, torch.Tensor) for a in args)
         assert log[0] == ("on", "side") and log[-1] == "off" and log[1:-2] == ["copy"] * copies
         assert log[-2].startswith("moe_pack_")
+
+
+def linear_tiling(T, N, K, T_max=None):
+    h = api.moe_linear_create(T if T_max is None else T_max, N, K)
+    try:
+        return api.moe_linear_tiling(h, T)
+    finally:
+        api.moe_linear_destroy(h)
+
+
+def test_linear_tiling_refusals():
+    L, n, split = api.lib(), ctypes.c_int(), ctypes.c_int()
+    h = api.moe_linear_create(64, 512, 256)
+    for args, code in (((None, 4, n, split), INVALID), ((h, -1, n, split), INVALID), ((h, 65, n, split), SHAPE),
+                       ((h, 4, None, split), INVALID), ((h, 4, n, None), INVALID), ((h, 0, n, split), 0), ((h, 64, n, split), 0)):
+        assert L.moe_linear_tiling(args[0], args[1], *(ctypes.byref(a) if a is not None else None for a in args[2:])) == code, args
+    api.moe_linear_destroy(h)
+
+
+@pytest.mark.parametrize("N", [256, 576, 1003, 1536, 4096, 7168])
+def test_linear_tiling_has_no_jump(N):
+    """One row more does not change how a prompt is cut, and narrow outputs use most of the 148 SMs at any length."""
+    K = 7168
+    assert linear_tiling(16, N, K) == (0, False)
+    assert linear_tiling(1025, N, K) == linear_tiling(1024, N, K)
+    for T in (1025, 2048, 4096, 8192):
+        rows, split = linear_tiling(T, N, K)
+        assert 16 <= rows <= 176 and rows % 16 == 0
+        tiles = -(-T // rows) * -(-N // 256)
+        assert split or tiles >= 96, (T, rows, tiles)
+
+
+def test_linear_tiling_keeps_the_steps_countable():
+    """Tiles of few rows would be more than 2^31 steps; the choice is among those that are not."""
+    T, N, K = 1 << 23, 1 << 20, 128
+    rows, split = linear_tiling(T, N, K)
+    assert -(-T // rows) * (N // 256) * (K // 128) < 1 << 31
