@@ -183,6 +183,38 @@ def test_linear_stays_inside_its_workspace(T):
     assert torch.equal(plan.forward(q, s, lin, dtype=torch.float32), y)
 
 
+@pytest.mark.parametrize("T, N, K, rows, split", [
+    (100, 20003, 128, 112, False), (333, 15003, 384, 176, False), (700, 20003, 384, 144, False), (340, 36003, 256, 176, False),
+    (65, 5003, 7168, 80, True), (129, 20003, 7168, 144, True), (331, 20003, 14336, 176, True),
+    (1777, 5003, 384, 128, False), (1500, 7169, 640, 160, False), (2110, 9003, 256, 176, False), (3001, 9003, 512, 160, False),
+    (1025, 255, 3584, 32, True), (2101, 1003, 1152, 64, False)])
+def test_linear_wide_tiles_and_long_prompts(T, N, K, rows, split):
+    """Tiles of more than 64 token rows, one and two atoms of token scales, whole and split, one and more a CTA, and past
+    1024 rows: against the oracle in both types, with guards behind the output and the workspace.  The weight rows repeat
+    with a period of 257, one more than a tile's, so that the oracle's product stays small."""
+    period = 257
+    x, base = randn((T, K), T, dtype=torch.bfloat16), randn((period, K), N, 0.02)
+    q, s = api.moe_quant_mxfp8(x)
+    lin, plan = api.LinearMXFP4(N, K), api.LinearPlan(T, N, K)
+    lin.pack(base[torch.arange(N, device="cuda") % period])
+    assert api.moe_linear_tiling(plan.handle, T) == (rows, split)    # of 148 SMs: what this case is here for
+    need, pad = api.moe_linear_workspace_bytes(plan.handle), 4096
+    ws = torch.full((need + (16 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    api.moe_linear_set_workspace(plan.handle, ws[:need])
+    X = mx.dequantize_mx(q.cpu().numpy(), s.cpu().numpy(), "e4m3")
+    W = mx.dequantize_mx(*mx.quantize_mx(base.double().cpu().numpy(), "e2m1"), "e2m1")
+    cols = np.arange(N) % period
+    ref, tol = X @ W.T, (K / 32 + 64 + 256) * 2.0 ** -23 * (np.abs(X) @ np.abs(W).T)
+    for dtype, half in ((torch.float32, 2.0 ** -24), (torch.bfloat16, 2.0 ** -8)):
+        bound = tol + half * (np.abs(ref) + tol) + 2.0 ** -133
+        buf = torch.full((T * N + pad,), 7, dtype=dtype, device="cuda")
+        y = plan.forward(q, s, lin, y=buf[:T * N].view(T, N))
+        assert plan.check()[0] == 0 and bool((buf[T * N:] == 7).all()) and bool((ws[need:] == 0x5A).all())
+        got = y.double().cpu().numpy()
+        assert np.all(np.abs(got - ref[:, cols]) <= bound[:, cols]), float((np.abs(got - ref[:, cols]) / bound[:, cols]).max())
+        assert torch.equal(plan.forward(q, s, lin, dtype=dtype), y)  # a fixed order of sums
+
+
 def test_linear_rows_do_not_depend_on_the_batch():
     """A row's result on the weight stream is the same alone and among seven others."""
     N, K = 777, 896
