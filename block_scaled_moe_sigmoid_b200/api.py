@@ -135,6 +135,8 @@ class _On:
     def __init__(self, index, stream):
         if index < 0:
             raise ValueError("expected CUDA tensors")
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"a stream of {stream.device} for tensors on CUDA device {index}")
         self.guards = [torch.cuda.device(index)] + ([torch.cuda.stream(stream)] if stream is not None else [])
 
     def __enter__(self):

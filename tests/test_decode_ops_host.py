@@ -1,6 +1,7 @@
 """Refusals of the operators around a decode step, without a GPU: every check stands before the
 first launch, so made-up pointers are never followed."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -213,3 +214,15 @@ def test_linear_tiling_keeps_the_steps_countable():
     T, N, K = 1 << 23, 1 << 20, 128
     rows, split = linear_tiling(T, N, K)
     assert -(-T // rows) * (N // 256) * (K // 128) < 1 << 31
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Not replaced by the current stream of the tensors' device."""
+    with pytest.raises(ValueError, match="cuda:1"):
+        api._On(0, SimpleNamespace(device=torch.device("cuda", 1)))
+    with pytest.raises(ValueError):
+        api._On(-1, None)
+    weights = SimpleNamespace(w=SimpleNamespace(get_device=lambda: 0), N=8, K=128)
+    other = SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="cuda:1"):
+        api.moe_linear_mxfp4(None, torch.zeros(1, 128, dtype=torch.uint8), torch.zeros(1, 4, dtype=torch.uint8), weights, stream=other)
