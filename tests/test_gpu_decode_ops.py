@@ -250,6 +250,33 @@ def test_linear_scales_at_the_ends_and_rows_that_are_not_finite(T):
     check_linear(q, s, w0, y)
 
 
+@pytest.mark.parametrize("T, N", [(5, 300), (16, 300), (40, 300), (100, 20003)])
+def test_linear_values_at_the_ends_of_the_scales(T, N):
+    """Rows and weights with the smallest scales and with large ones, against the oracle (the last case in tiles of 112 rows).
+    Below 2^-126 an fp32 value is a multiple of 2^-149: each of a sum's additions may round there by that much more."""
+    K, period = 512, 129
+    x, base = randn((T, K), 3, dtype=torch.bfloat16), randn((period, K), 4, 0.02)
+    base[6] *= 2.0 ** 60
+    base[7] *= 2.0 ** -100
+    base[8] *= 2.0 ** -125
+    q, s = api.moe_quant_mxfp8(x)
+    s[0] = 0                              # 2^-127
+    s[1, ::2] = 1
+    s[3] = 120                            # 2^-7 in all blocks
+    s[4, 3] = 180                         # one block that outweighs the others by 2^50
+    lin, plan = api.LinearMXFP4(N, K), api.LinearPlan(T, N, K)
+    lin.pack(base[torch.arange(N, device="cuda") % period])
+    y = plan.forward(q, s, lin, dtype=torch.float32).double().cpu().numpy()
+    assert plan.check()[0] == 0
+    X = mx.dequantize_mx(q.cpu().numpy(), s.cpu().numpy(), "e4m3")
+    W = mx.dequantize_mx(*mx.quantize_mx(base.double().cpu().numpy(), "e2m1"), "e2m1")
+    cols, terms = np.arange(N) % period, K / 32 + 64 + 256
+    ref, tol = X @ W.T, terms * 2.0 ** -23 * (np.abs(X) @ np.abs(W).T)
+    bound = tol + 2.0 ** -24 * (np.abs(ref) + tol) + terms * 2.0 ** -149
+    assert np.all(np.abs(y - ref[:, cols]) <= bound[:, cols]), float((np.abs(y - ref[:, cols]) / bound[:, cols]).max())
+    assert np.count_nonzero(y[0]) > N // 2     # the smallest scale is not taken for zero
+
+
 @pytest.mark.parametrize("T, dtype", [(3, torch.float32), (8, torch.bfloat16), (20, torch.bfloat16), (100, torch.float32)])
 def test_linear_writes_its_rows_only(T, dtype):
     N, K, pad = 1003, 256, 512
