@@ -66,13 +66,14 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return cudaErrorInvalidDevice;
-    const int team = ((nvec + 1) / 2 + 31) / 32 * 32, grid = sms * std::max(1, 1152 / team);   // as many as fit (56 registers a thread)
-    if (nvec > (RES == NORM_RES_BF16 ? kNormStreamVecs : kNormStreamVecsPlain) && nvec <= 2048 && a.rows > grid) {
-      auto kern = add_rmsnorm_mxfp8_stream_kernel<RES, 2>;
+    constexpr int V = kNormStreamVecsPerThread;
+    const int team = ((nvec + V - 1) / V + 31) / 32 * 32, grid = sms * std::max(1, 1152 / team);   // as many as fit (56 registers a thread)
+    if (nvec > (RES == NORM_RES_BF16 ? kNormStreamVecs : kNormStreamVecsPlain) && nvec <= 1024 * V && a.rows > grid) {
+      auto kern = add_rmsnorm_mxfp8_stream_kernel<RES>;
       static std::atomic<uint64_t> done{0};
-      const cudaError_t e = ensure_smem_attr(kern, kNormDepth * 2 * 32 * 1024, done);
+      const cudaError_t e = ensure_smem_attr(kern, kNormDepth * V * 32 * 1024, done);
       if (e != cudaSuccess) return e;
-      return launch_k(kern, grid, team, kNormDepth * 2 * (RES == NORM_RES_BF16 ? 32 : 16) * team, s, a);
+      return launch_k(kern, grid, team, kNormDepth * V * (RES == NORM_RES_BF16 ? 32 : 16) * team, s, a);
     }
   }
   if (nvec > 2048) return launch_norm_rows<RES, 4>(a, s);

@@ -167,13 +167,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormArgs 
 // 8192 x 7168 with a bf16 residual: 85.6 us, 6.2 TB/s, where a CTA per row takes 96 us (its loads stop
 // while it reduces and stores).  With an fp32 residual a CTA per row has enough loads in flight (117 us,
 // 6.5 TB/s) and the ring would hold too few rows (134 us).
-constexpr int kNormDepth = 3;
+constexpr int kNormDepth = 3, kNormStreamVecsPerThread = 2;
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-template <int RES, int V>
+template <int RES>
 __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_stream_kernel(const NormArgs a) {
   static_assert(RES != NORM_RES_F32, "fp32 residuals take a CTA per row");
+  constexpr int V = kNormStreamVecsPerThread;
   constexpr int PIECES = RES == NORM_RES_BF16 ? 2 : 1;   // 16-byte pieces of a vector: x, residual
   extern __shared__ uint4 ring[];                        // [kNormDepth][V][PIECES][threads]
   __shared__ float part[2][32];
