@@ -106,7 +106,7 @@ constexpr int kLinearSmall = 64, kLinearWide = 176;
 //   1024 rows of 28672 x 7168, 233 instead of 197).
 // Fitted to ten shapes from 256 x 7168 to 28672 x 7168 with 17 to 8192 rows, every height and both forms
 // timed: the choice takes 1.1% more than the best one on average.  300 rows of 7168 x 7168: five whole
-// tiles of 64 rows by 28 take 20.9 us, 64 rows: one tile split 13.4, two whole ones 19.5.
+// tiles of 64 rows by 28 take 20.9 us, 64 rows: one tile split 13.4, two whole ones 20.2.
 struct LinearPick { int n_per, unit; };
 LinearPick pick_linear_tiles(int T, int m_tiles, int k_tiles, int grid) {
   LinearPick best = {kLinearWide, k_tiles};

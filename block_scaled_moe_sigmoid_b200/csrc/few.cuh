@@ -37,10 +37,11 @@
 // each operand goes to its uniform register by itself, and the scale warp alone then held the stream at
 // 5.9 TB/s.
 //
-// Measured (B200, copy rate 6.54 TB/s): 8 tokens on 58 experts of 3584 x 3072 in 150 us, 6.7 TB/s; one
-// token on 16 experts of 7168 x 3072 in 91.0 us, 6.2 TB/s (111 us with a shared expert); 8 rows of
-// 40000 x 7168 in 26.9 us, 5.7 TB/s.  Around the stream each kernel takes about 4 us for its tables, the
-// first load's latency and the last exchange; small shapes are that latency.
+// Measured (B200, copy rate 6.54 TB/s; replayed on one set of weights): 8 tokens on 57 experts of 3584 x 3072
+// in 150 us, 6.7 TB/s; one token on 16 experts of 7168 x 3072 in 91.0 us, 6.2 TB/s (112 us with a shared
+// expert, 115 over three sets of weights); 8 rows of 40000 x 7168 in 26.9 us, 5.7 TB/s.  Around the stream
+// each kernel takes about 4 us for its tables, the first load's latency and the last exchange; small shapes
+// are that latency.
 #pragma once
 #include <type_traits>
 

@@ -2,13 +2,18 @@
 //
 // A tile is 256 weight rows x up to NB token rows, its contraction K / 128 steps; a step loads 16 KB of
 // codes (the tensor core reads E2M1 and E4M3 with one E8M0 scale per 32 elements) and the token rows.
-// A prompt of a few hundred rows makes 28 to 112 tiles at N = 7168, too few for 148 SMs to take whole
-// ones: as in few.cuh the list of steps is then cut evenly, and fp32 partials are exchanged.  Here a
-// second kernel adds them, in the order of the CTAs: a tile's partials are up to 160 KB each, and one
-// CTA reading five of them takes longer than the products (39 us for 160 x 7168 x 7168).
+// Up to 128 token rows make 28 or 56 tiles at N = 7168, and narrow outputs few at any length: too few for
+// 148 SMs to take whole ones.  As in few.cuh the list of steps is then cut evenly, and fp32 partials are
+// exchanged.  Here a second kernel adds them, in the order of the CTAs: a tile's partials are up to 176 KB
+// each, and one CTA reading five of them takes longer than the products (39 us for 160 x 7168 x 7168,
+// 19.5 with the second kernel).
 //
-// Bound by the MMAs from about 100 rows per tile on (eight of N / 2 cycles per step), by the weight
-// stream below.  Roles as in few.cuh, and warp 13, which makes the token scales' atoms.
+// Bound, with tiles of up to 64 rows, by the issue of the MMAs and the weight stream (eight MMAs of 64
+// columns take 384 of about 460 cycles a step), with higher ones by the rate at which shared memory fills.
+// Measured (B200, weights from memory; in a short run, and without a pause): 7168 x 7168 with 64 rows
+// 13.0 and 13.4 us, 300 rows 20.7 and 23.0, 1024 rows 50.2 and 59.8, 4096 rows 163 and 197 (2.6 and 2.1
+// PFLOP/s).  Roles as in few.cuh, and warp 13, which makes the token
+// scales' atoms.
 #pragma once
 #include "few.cuh"
 
